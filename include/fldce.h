@@ -334,6 +334,150 @@ int fldce_forward(fldce_handle h,
                   int32_t* err_count, void* stream);
 
 /*
+ * Token log-probabilities of a language-model head: what scoring, decoding
+ * and policy-gradient training ask of the same H, W and bias the loss takes.
+ * With z = s (H W^T + b) and p = softmax(z), for every token n:
+ *
+ *   lse[n]      = log sum_v exp z[n,v]
+ *   logprob[n]  = z[n, y_n] - lse[n]            (0 for an ignored token)
+ *   entropy[n]  = lse[n] - sum_v p[n,v] z[n,v]
+ *   top_ids[n]  = the top_k columns with the largest z, best first; equal
+ *                 values in increasing column order
+ *   top_logprobs[n] = their z - lse[n]
+ *
+ * The logits never reach memory.  The order of top_ids is that of the exact
+ * dot products (candidates are recomputed in fp64), so it does not depend on
+ * N or on how the work is split.  A bias of -inf (or of the type's lowest
+ * value) takes a column out: its p is 0.  A row whose every logit is -inf has
+ * lse = -inf, entropy 0, logprob -inf and, in the gradient, a row of zeros.
+ * Alternatives that do not exist (fewer than top_k logits above -inf) read
+ * id -1 and log-probability -inf.  A row with a NaN or +inf logit has NaN
+ * results and no meaningful ids.
+ *
+ * The plan gives dtype, D, V, max_N, logit_scale, ignore_index and, for the
+ * gradient, chunk_N and the flags DW_FP32, DH_FP32 and DW_ACCUMULATE;
+ * label_smoothing is not used.  Plans that are vocabulary shards or have
+ * SKIP_IGNORED or FUSED_DH are refused (UNSUPPORTED).
+ *
+ * fldce_logprob_call: zero-initialise and set what is needed.
+ *   H        [device, in] [N, D] dtype.
+ *   W        [device, in] [V, D] dtype; or NULL with w4 set:
+ *   w4, w4_scales, w4_group  [device, in] a 4-bit weight (see
+ *            fldce_w4_quantize); dtype has to be FLDCE_BF16.
+ *   bias     [device, in, may be NULL] [V] dtype, 16-byte aligned.
+ *   token    [device, in, may be NULL] [N] int64: y.  ignore_index, or an id
+ *            outside [0, V) (counted in err_count[0]), has logprob 0.
+ *   top_k    0 to FLDCE_MAX_TOP_K, at most V.
+ *   logprob, entropy, lse  [device, out, each may be NULL] [N] fp32; logprob
+ *            needs token.
+ *   top_ids [device, out] [N, top_k] int32, top_logprobs [N, top_k] fp32;
+ *            required when top_k > 0.
+ *   workspace  [device] at least fldce_logprob_workspace_size bytes, 256-byte
+ *            aligned; the remarks on fldce_fwd_bwd's workspace apply.
+ *   err_count  [device, out, may be NULL] as for fldce_fwd_bwd.
+ *   stream   as for fldce_fwd_bwd; the call may be captured.
+ * N == 0 is allowed and writes no per-token output.
+ * Errors: INVALID_ARG, UNSUPPORTED, ALIGN, WORKSPACE, DEVICE, CUDA.
+ */
+#define FLDCE_MAX_TOP_K 20
+typedef struct {
+    const void* H;
+    const void* W;
+    const void* w4;
+    const void* w4_scales;
+    const void* bias;
+    const int64_t* token;
+    int64_t N;
+    int32_t w4_group;
+    int32_t top_k;
+    float* logprob;
+    float* entropy;
+    float* lse;
+    int32_t* top_ids;
+    float* top_logprobs;
+    void* workspace;
+    size_t workspace_bytes;
+    int32_t* err_count;
+    void* stream;
+} fldce_logprob_call;
+
+/* fldce_logprob_workspace_size -- workspace bytes of fldce_logprob for N
+ * tokens and top_k alternatives (either kind of weight).
+ * Errors: INVALID_ARG, UNSUPPORTED (plan). */
+int fldce_logprob_workspace_size(fldce_handle h, int64_t N, int32_t top_k, size_t* bytes);
+
+int fldce_logprob(fldce_handle h, const fldce_logprob_call* call);
+
+/*
+ * fldce_logprob_bwd -- gradients of sum_n dlogprob[n] logprob[n] +
+ * dentropy[n] entropy[n]: with a = dlogprob (0 for an ignored token) and
+ * e = dentropy,
+ *   G[n,v] = s (p[n,v] (-(a + e entropy[n]) - e log p[n,v]) + a [v = y_n])
+ *   dH = G W,  dW = G^T H,  db = sum_n G[n,:].
+ * G is rounded once to the dtype, as in the loss's gradient.
+ *   H, W, bias, token   as given to fldce_logprob (a 16- or 32-bit weight).
+ *   lse, entropy        [device, in] [N] fp32, its results (entropy may be
+ *                       NULL without dentropy).
+ *   dlogprob, dentropy  [device, in, each may be NULL = 0] [N] fp32; what
+ *                       dlogprob holds at ignored tokens is not read.
+ *   dH, dW, db          [device, out] as for fldce_fwd_bwd_ex; each may be
+ *                       NULL when it is not needed (one has to be set).
+ *   workspace           at least fldce_workspace_size(h, N) bytes.
+ *   err_count, stream   as above.
+ * N == 0 writes dW = 0 and db = 0 (nothing with DW_ACCUMULATE).
+ * Errors: INVALID_ARG, UNSUPPORTED, ALIGN, WORKSPACE, DEVICE, CUDA.
+ */
+typedef struct {
+    const void* H;
+    const void* W;
+    const void* bias;
+    const int64_t* token;
+    int64_t N;
+    const float* lse;
+    const float* entropy;
+    const float* dlogprob;
+    const float* dentropy;
+    void* dH;
+    void* dW;
+    void* db;
+    void* workspace;
+    size_t workspace_bytes;
+    int32_t* err_count;
+    void* stream;
+} fldce_logprob_grad_call;
+
+int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* call);
+
+/*
+ * 4-bit head weight: W[v, d] = q[v, d] * scale[v, d / group] with q a two's
+ * complement nibble in [-8, 7].
+ *   packed [V, D/2] bytes, row-major, 16-byte aligned: byte i of a row holds
+ *          element 2i in its low half and element 2i + 1 in its high half;
+ *   scales [V, ceil(D / group)] bf16, row-major;
+ *   group  32, 64 or 128 (the last group of a row may be short); D % 32 == 0.
+ *
+ * fldce_w4_quantize -- round a weight of `dtype` to it: scale = bf16(max |w|
+ * / 7) over the group, q = round-to-nearest-even(w / scale) clamped to
+ * [-7, 7]; a group of zeros has scale 0.  The weights have to be finite.
+ * Errors: INVALID_ARG, UNSUPPORTED (dtype, group, D), ALIGN, DEVICE, CUDA.
+ */
+int fldce_w4_quantize(const void* W, int32_t dtype, int64_t V, int64_t D, int32_t group,
+                      void* packed, void* scales, void* stream);
+
+/*
+ * fldce_w4_linear -- logits of a few tokens: out[n, v] = <x[n], W[v]> (+
+ * bias[v]), summed in fp32 and rounded once to out_dtype.
+ *   x [device, in] [N, D] bf16, 16-byte aligned; bias [V] bf16 or NULL;
+ *   out [device, out] [N, V] of out_dtype (FLDCE_BF16 or FLDCE_FP32).
+ * The weight is read once for every few tokens; with many tokens a 16-bit
+ * weight and a dense product are faster.
+ * Errors: INVALID_ARG, UNSUPPORTED, ALIGN, DEVICE, CUDA.
+ */
+int fldce_w4_linear(const void* x, int64_t N, const void* packed, const void* scales, int32_t group,
+                    const void* bias, int64_t V, int64_t D, void* out, int32_t out_dtype,
+                    void* stream);
+
+/*
  * Optional profiling window: per-kernel device time over a window of calls.
  * fldce_profile_begin(h, max_calls) creates CUDA events (no device memory)
  * for the next `max_calls` calls on this handle; each of those calls records

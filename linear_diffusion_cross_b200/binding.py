@@ -40,8 +40,11 @@ EXPORTS = ("fldce_create", "fldce_workspace_size", "fldce_chunk_size", "fldce_fw
            "fldce_fwd_bwd_noalloc", "fldce_forward", "fldce_fwd_bwd_ex", "fldce_forward_ex",
            "fldce_count_valid", "fldce_vp_stats", "fldce_vp_fwd_bwd",
            "fldce_profile_begin", "fldce_profile_end", "fldce_profile_kind_name",
+           "fldce_logprob_workspace_size", "fldce_logprob", "fldce_logprob_bwd",
+           "fldce_w4_quantize", "fldce_w4_linear",
            "fldce_scale", "fldce_selftest_wait", "fldce_destroy", "fldce_strerror", "fldce_version")
 FLDCE_PROF_KINDS = 9
+FLDCE_MAX_TOP_K = 20
 
 
 class FldceError(RuntimeError):
@@ -89,6 +92,50 @@ class fldce_call(ctypes.Structure):
         ("err_count", ctypes.c_void_p),
         ("stream", ctypes.c_void_p),
         ("dw_ready_event", ctypes.c_void_p),
+    ]
+
+
+class fldce_logprob_call(ctypes.Structure):
+    _fields_ = [
+        ("H", ctypes.c_void_p),
+        ("W", ctypes.c_void_p),
+        ("w4", ctypes.c_void_p),
+        ("w4_scales", ctypes.c_void_p),
+        ("bias", ctypes.c_void_p),
+        ("token", ctypes.c_void_p),
+        ("N", ctypes.c_int64),
+        ("w4_group", ctypes.c_int32),
+        ("top_k", ctypes.c_int32),
+        ("logprob", ctypes.c_void_p),
+        ("entropy", ctypes.c_void_p),
+        ("lse", ctypes.c_void_p),
+        ("top_ids", ctypes.c_void_p),
+        ("top_logprobs", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+        ("err_count", ctypes.c_void_p),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
+class fldce_logprob_grad_call(ctypes.Structure):
+    _fields_ = [
+        ("H", ctypes.c_void_p),
+        ("W", ctypes.c_void_p),
+        ("bias", ctypes.c_void_p),
+        ("token", ctypes.c_void_p),
+        ("N", ctypes.c_int64),
+        ("lse", ctypes.c_void_p),
+        ("entropy", ctypes.c_void_p),
+        ("dlogprob", ctypes.c_void_p),
+        ("dentropy", ctypes.c_void_p),
+        ("dH", ctypes.c_void_p),
+        ("dW", ctypes.c_void_p),
+        ("db", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+        ("err_count", ctypes.c_void_p),
+        ("stream", ctypes.c_void_p),
     ]
 
 
@@ -140,6 +187,18 @@ def load() -> ctypes.CDLL:
     lib.fldce_vp_fwd_bwd.restype = ctypes.c_int
     lib.fldce_count_valid.argtypes = [_P, _P, _I64, _P, _P]
     lib.fldce_count_valid.restype = ctypes.c_int
+    lib.fldce_logprob_workspace_size.argtypes = [_P, _I64, ctypes.c_int32,
+                                                 ctypes.POINTER(ctypes.c_size_t)]
+    lib.fldce_logprob_workspace_size.restype = ctypes.c_int
+    lib.fldce_logprob.argtypes = [_P, ctypes.POINTER(fldce_logprob_call)]
+    lib.fldce_logprob.restype = ctypes.c_int
+    lib.fldce_logprob_bwd.argtypes = [_P, ctypes.POINTER(fldce_logprob_grad_call)]
+    lib.fldce_logprob_bwd.restype = ctypes.c_int
+    lib.fldce_w4_quantize.argtypes = [_P, ctypes.c_int32, _I64, _I64, ctypes.c_int32, _P, _P, _P]
+    lib.fldce_w4_quantize.restype = ctypes.c_int
+    lib.fldce_w4_linear.argtypes = [_P, _I64, _P, _P, ctypes.c_int32, _P, _I64, _I64, _P,
+                                    ctypes.c_int32, _P]
+    lib.fldce_w4_linear.restype = ctypes.c_int
     lib.fldce_selftest_wait.argtypes = [_I64, _P, _P]
     lib.fldce_selftest_wait.restype = ctypes.c_int
     lib.fldce_scale.argtypes = [_P, _I64, ctypes.c_int32, _P, _P]
@@ -294,6 +353,54 @@ def fldce_vp_fwd_bwd(h, call: fldce_call, all_stats, n_shards: int) -> int:
 def fldce_count_valid(h, target, N, count, stream=None) -> int:
     return _check(load().fldce_count_valid(h, _ptr(target), int(N), _ptr(count),
                                            _stream(stream)), "fldce_count_valid")
+
+
+def _fill(c, kw):
+    for k, v in kw.items():
+        if k == "stream":
+            c.stream = _stream(v)
+        elif k in ("N", "w4_group", "top_k", "workspace_bytes"):
+            setattr(c, k, int(v))
+        else:
+            setattr(c, k, _ptr(v))
+    return c
+
+
+def make_logprob_call(**kw) -> fldce_logprob_call:
+    """A zero-initialised fldce_logprob_call; tensors become device pointers."""
+    return _fill(fldce_logprob_call(), kw)
+
+
+def make_logprob_grad_call(**kw) -> fldce_logprob_grad_call:
+    """A zero-initialised fldce_logprob_grad_call; tensors become device pointers."""
+    return _fill(fldce_logprob_grad_call(), kw)
+
+
+def fldce_logprob_workspace_size(h, N: int, top_k: int) -> int:
+    ws = ctypes.c_size_t()
+    _check(load().fldce_logprob_workspace_size(h, int(N), int(top_k), ctypes.byref(ws)),
+           "fldce_logprob_workspace_size")
+    return ws.value
+
+
+def fldce_logprob(h, call: fldce_logprob_call) -> int:
+    return _check(load().fldce_logprob(h, ctypes.byref(call)), "fldce_logprob")
+
+
+def fldce_logprob_bwd(h, call: fldce_logprob_grad_call) -> int:
+    return _check(load().fldce_logprob_bwd(h, ctypes.byref(call)), "fldce_logprob_bwd")
+
+
+def fldce_w4_quantize(W, dtype, V, D, group, packed, scales, stream=None) -> int:
+    return _check(load().fldce_w4_quantize(_ptr(W), int(dtype), int(V), int(D), int(group),
+                                           _ptr(packed), _ptr(scales), _stream(stream)),
+                  "fldce_w4_quantize")
+
+
+def fldce_w4_linear(x, N, packed, scales, group, bias, V, D, out, out_dtype, stream=None) -> int:
+    return _check(load().fldce_w4_linear(_ptr(x), int(N), _ptr(packed), _ptr(scales), int(group),
+                                         _ptr(bias), int(V), int(D), _ptr(out), int(out_dtype),
+                                         _stream(stream)), "fldce_w4_linear")
 
 
 def fldce_scale(x, n, dtype, g, stream=None) -> int:

@@ -35,6 +35,8 @@
 #include "../../include/fldce.h"
 #include "fused_gdh.cuh"
 #include "kernels.cuh"
+#include "logprob.cuh"
+#include "w4.cuh"
 
 using namespace fldce;
 
@@ -441,6 +443,95 @@ int check_device(DeviceInfo* d) {
     return FLDCE_OK;
 }
 
+// FLDCE_CUDA: return from the enclosing function on a CUDA error.
+#define FLDCE_CUDA(x)                                  \
+    do {                                               \
+        if ((x) != cudaSuccess) return FLDCE_ERR_CUDA; \
+    } while (0)
+
+// The two bf16 gradient products of one chunk of `rows` tokens from its G.
+struct GradGemm {
+    fldce_plan* h;
+    const Layout* L;
+    uint8_t* ws;
+    Counters* cnt;
+    const DeviceInfo* dev;
+    cudaStream_t st;
+    int rows;
+    int64_t r0;               // first token of the chunk
+    DynRows dyn;              // compacted rows (dim is set per product)
+
+    // dH = G W (K = V).  When one pass over the tiles leaves many SMs
+    // idle in its last round, the vocabulary is split into k ranges;
+    // split j stores its fp32 partial in its own buffer and one pass
+    // sums them in split order (deterministic) into dH.
+    int dh(const CUtensorMap& mG_k, const CUtensorMap& mW_mn, void* dH) const {
+        const int64_t D = h->cfg.D, V = h->cfg.V;
+        const DhPlan dp = plan_dh(rows, D, V, std::max(1, dev->sms / 2));
+        const int ks = dp.k_splits;
+        StoreEpi::Params hp;
+        const bool dh_fp32 = (h->cfg.flags & FLDCE_FLAG_DH_FP32) != 0;
+        float* part = reinterpret_cast<float*>(ws + L->dh_acc);
+        const int split_rows = (int)round_up((size_t)rows, 256);
+        void* dHc = static_cast<uint8_t*>(dH) + (size_t)r0 * D * (dh_fp32 ? 4 : 2);
+        if (ks > 1) {
+            if (!make_store_map(&hp.omap, part, D, (uint64_t)ks * split_rows, D, 4))
+                return FLDCE_ERR_CUDA;
+            hp.mode = WS_STORE;
+            hp.split_rows = split_rows;
+        } else if (dh_fp32) {
+            if (!make_store_map(&hp.omap, dHc, D, rows, D, 4)) return FLDCE_ERR_CUDA;
+            hp.mode = WS_STORE;
+        } else {
+            if (!make_store_map(&hp.omap, dHc, D, rows, D, 2)) return FLDCE_ERR_CUDA;
+            hp.mode = OUT_BF16;
+        }
+        const Walk dh_walk{1, ks, kOneBlock};
+        const DynRows dr{dyn.count, dyn.base, 1};
+        if (dp.wide)
+            FLDCE_CUDA((launch_gemm<CfgKM2, StoreEpi>(mG_k, mW_mn, rows, D, V, dh_walk, hp,
+                                                      &cnt->dev_err, dev->sms, st, dr)));
+        else
+            FLDCE_CUDA((launch_gemm<CfgKM, StoreEpi>(mG_k, mW_mn, rows, D, V, dh_walk, hp,
+                                                     &cnt->dev_err, dev->sms, st, dr)));
+        prof_mark(h, PK_DH, st);
+        if (ks > 1) {
+            FLDCE_CUDA(launch_sum_splits(part, (int64_t)split_rows * D, ks, dHc, !dh_fp32,
+                                         (int64_t)rows * D, dev->sms, st));
+            prof_mark(h, PK_CONVERT, st);
+        }
+        return FLDCE_OK;
+    }
+
+    // dW = G^T H (K = tokens of the chunk): one chunk writes dW directly;
+    // several store, then reduce-add, fp32 partial sums.
+    int dw(const CUtensorMap& mG_mn, const CUtensorMap& mH_mn, void* dW, int64_t ci) const {
+        const int64_t D = h->cfg.D, V = h->cfg.V;
+        const bool fp32_dw = dw_out_fp32(h), accum = dw_accumulate(h);
+        float* dw_ws = fp32_dw ? static_cast<float*>(dW) : reinterpret_cast<float*>(ws + L->dw_acc);
+        StoreEpi::Params wp;
+        if (L->nchunks == 1 && !fp32_dw && !accum) {
+            if (!make_store_map(&wp.omap, dW, D, V, D, 2)) return FLDCE_ERR_CUDA;
+            wp.mode = OUT_BF16;
+        } else {
+            // fp32 partial sums; an fp32 dW accumulated into takes
+            // every chunk's reduce-add directly
+            if (!make_store_map(&wp.omap, dw_ws, D, V, D, 4)) return FLDCE_ERR_CUDA;
+            wp.mode = (ci == 0 && !(accum && fp32_dw)) ? WS_STORE : WS_ADD;
+        }
+        const Walk dw_walk{1, 1, kOneBlock};
+        FLDCE_CUDA((launch_gemm<CfgMM, StoreEpi>(mG_mn, mH_mn, (int)V, D, rows, dw_walk, wp,
+                                                 &cnt->dev_err, dev->sms, st,
+                                                 DynRows{dyn.count, dyn.base, 2})));
+        prof_mark(h, PK_DW, st);
+        if ((L->nchunks > 1 || accum) && !fp32_dw && ci + 1 == L->nchunks) {
+            FLDCE_CUDA(launch_to_bf16(dw_ws, dW, V * D, accum, dev->sms, st));
+            prof_mark(h, PK_CONVERT, st);
+        }
+        return FLDCE_OK;
+    }
+};
+
 // The shared body of fldce_fwd_bwd and fldce_forward.
 // mode: MERGE_LOCAL (the whole vocabulary in this plan), MERGE_EMIT_STATS
 // (a shard's sweep 1 and statistics only), MERGE_GATHERED (a shard's
@@ -527,11 +618,6 @@ int run(fldce_handle h, const fldce_call& call, bool backward, int mode = MERGE_
     const int32_t* dynp = nullptr;           // device-side row count of the compacted tokens
     const float s = cfg.logit_scale, eps = cfg.label_smoothing;
     const float c = s * 1.4426950408889634f;
-
-#define FLDCE_CUDA(x)                                  \
-    do {                                               \
-        if ((x) != cudaSuccess) return FLDCE_ERR_CUDA; \
-    } while (0)
 
     FLDCE_CUDA(cudaMemsetAsync(cnt, 0, sizeof(Counters), st));
     prof_mark(h, PK_GAP, st);
@@ -728,10 +814,7 @@ int run(fldce_handle h, const fldce_call& call, bool backward, int mode = MERGE_
             const void* Hc = static_cast<const __nv_bfloat16*>(H) + r0 * D;
             if (!make_map(&mH_mn, Hc, D, rows, D, 64, 64)) return FLDCE_ERR_CUDA;
 
-            // dH = G W (K = V).  When one pass over the tiles leaves many SMs
-            // idle in its last round, the vocabulary is split into k ranges;
-            // split j stores its fp32 partial in its own buffer and one pass
-            // sums them in split order (deterministic) into dH.
+            const GradGemm gg{h, &L, ws, cnt, &dev, st, rows, r0, DynRows{dynp, (int)r0, 1}};
             auto do_dh = [&]() -> int {
                 if (fused_dh) {
                     // the fused kernel left dH in fp32: round (or copy) it out
@@ -742,67 +825,9 @@ int run(fldce_handle h, const fldce_call& call, bool backward, int mode = MERGE_
                     prof_mark(h, PK_CONVERT, st);
                     return FLDCE_OK;
                 }
-                const DhPlan dp = plan_dh(rows, D, V, std::max(1, dev.sms / 2));
-                const bool wide = dp.wide;
-                const int ks = dp.k_splits;
-                StoreEpi::Params hp;
-                const bool dh_fp32 = (cfg.flags & FLDCE_FLAG_DH_FP32) != 0;
-                float* part = reinterpret_cast<float*>(ws + L.dh_acc);
-                const int split_rows = (int)round_up((size_t)rows, 256);
-                void* dHc = static_cast<uint8_t*>(dH) + (size_t)r0 * D * (dh_fp32 ? 4 : 2);
-                if (ks > 1) {
-                    if (!make_store_map(&hp.omap, part, D, (uint64_t)ks * split_rows, D, 4))
-                        return FLDCE_ERR_CUDA;
-                    hp.mode = WS_STORE;
-                    hp.split_rows = split_rows;
-                } else if (dh_fp32) {
-                    if (!make_store_map(&hp.omap, dHc, D, rows, D, 4)) return FLDCE_ERR_CUDA;
-                    hp.mode = WS_STORE;
-                } else {
-                    if (!make_store_map(&hp.omap, dHc, D, rows, D, 2)) return FLDCE_ERR_CUDA;
-                    hp.mode = OUT_BF16;
-                }
-                const Walk dh_walk{1, ks, kOneBlock};
-                if (wide)
-                    FLDCE_CUDA((launch_gemm<CfgKM2, StoreEpi>(mG_k, mW_mn, rows, D, V, dh_walk,
-                                                              hp, &cnt->dev_err, dev.sms, st,
-                                                              DynRows{dynp, (int)r0, 1})));
-                else
-                    FLDCE_CUDA((launch_gemm<CfgKM, StoreEpi>(mG_k, mW_mn, rows, D, V, dh_walk,
-                                                             hp, &cnt->dev_err, dev.sms, st,
-                                                             DynRows{dynp, (int)r0, 1})));
-                prof_mark(h, PK_DH, st);
-                if (ks > 1) {
-                    FLDCE_CUDA(launch_sum_splits(part, (int64_t)split_rows * D, ks, dHc,
-                                                 !dh_fp32, (int64_t)rows * D, dev.sms, st));
-                    prof_mark(h, PK_CONVERT, st);
-                }
-                return FLDCE_OK;
+                return gg.dh(mG_k, mW_mn, dH);
             };
-            // dW = G^T H (K = tokens of the chunk): one chunk writes dW
-            // directly; several store, then reduce-add, fp32 partial sums.
-            auto do_dw = [&]() -> int {
-                StoreEpi::Params wp;
-                if (L.nchunks == 1 && !fp32_dw && !accum) {
-                    if (!make_store_map(&wp.omap, dW, D, V, D, 2)) return FLDCE_ERR_CUDA;
-                    wp.mode = OUT_BF16;
-                } else {
-                    // fp32 partial sums; an fp32 dW accumulated into takes
-                    // every chunk's reduce-add directly
-                    if (!make_store_map(&wp.omap, dw_ws, D, V, D, 4)) return FLDCE_ERR_CUDA;
-                    wp.mode = (ci == 0 && !(accum && fp32_dw)) ? WS_STORE : WS_ADD;
-                }
-                const Walk dw_walk{1, 1, kOneBlock};
-                FLDCE_CUDA((launch_gemm<CfgMM, StoreEpi>(mG_mn, mH_mn, (int)V, D, rows, dw_walk,
-                                                         wp, &cnt->dev_err, dev.sms, st,
-                                                         DynRows{dynp, (int)r0, 2})));
-                prof_mark(h, PK_DW, st);
-                if ((L.nchunks > 1 || accum) && !fp32_dw && ci + 1 == L.nchunks) {
-                    FLDCE_CUDA(launch_to_bf16(dw_ws, dW, V * D, accum, dev.sms, st));
-                    prof_mark(h, PK_CONVERT, st);
-                }
-                return FLDCE_OK;
-            };
+            auto do_dw = [&]() -> int { return gg.dw(mG_mn, mH_mn, dW, ci); };
             if (dw_first) {
                 if (int e = do_dw()) return e;
                 FLDCE_CUDA(cudaEventRecord(reinterpret_cast<cudaEvent_t>(call.dw_ready_event), st));
@@ -856,11 +881,12 @@ int run(fldce_handle h, const fldce_call& call, bool backward, int mode = MERGE_
     k_finish<<<1, 1024, 0, st>>>(loss_tok, N, cnt, loss, err_count);
     FLDCE_CUDA(cudaGetLastError());
     prof_mark(h, PK_FINISH, st);
-#undef FLDCE_CUDA
     return FLDCE_OK;
 }
 
 }  // namespace
+
+#include "logprob_host.cuh"
 
 extern "C" {
 

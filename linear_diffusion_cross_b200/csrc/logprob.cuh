@@ -1,0 +1,650 @@
+// logprob.cuh -- device code of the token log-probabilities: log p of given
+// tokens, entropy, the best alternatives, and the gradient of both.
+//
+// With z = s (x W^T + b) and p = softmax(z):
+//   lse = log sum_v e^(z_v),  logprob = z_y - lse,  entropy = lse - sum_v p_v z_v.
+// Any slice of the vocabulary is summarised by
+//   m = max a,  l = sum 2^d,  w = sum 2^d d,   a = sign(s) (x W^T + b),  d = c (a - m),
+//   c = |s| log2(e),
+// and slices merge exactly: with f = 2^(c (m - M)), l -> f l and
+// w -> f (w + c (m - M) l).  At the end lse = c M ln 2 + ln l and
+// entropy = ln l - ln 2 w / l, a difference of small numbers (lse - sum p z
+// would cancel).  The maximum is taken before the scale, so that logits of
+// the type's lowest value keep their differences instead of overflowing.
+//
+// The alternatives' order is decided in 64 bits: every slice keeps its KC best
+// columns by the fp32 accumulator, the merge keeps the KC best of all slices
+// (KC exceeds the k asked for by 3 or more), recomputes those columns' dot
+// products in fp64 and sorts by (value, lowest id).  So ids do not depend on
+// the summation order of the matrix instructions, the tile that computed
+// them, or the number of tokens in the call.
+#pragma once
+#include "kernels.cuh"
+
+namespace fldce {
+
+constexpr float kNegInf = -__builtin_huge_valf();
+
+// Candidates kept per slice for k alternatives.
+constexpr int candidates_for(int k) { return k == 0 ? 0 : (k == 1 ? 4 : (k <= 5 ? 8 : 24)); }
+
+// Order-preserving map of floats to unsigned integers (0 is below every float).
+__device__ __forceinline__ uint32_t float_key(float x) {
+    const uint32_t u = __float_as_uint(x);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float key_float(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+
+// The running (m, l, w) of one row over a slice, fed in groups of values.
+struct RunningStats {
+    float m = kNegInf, l = 0.f, w = 0.f;
+
+    // Move the reference to nm >= m; returns the finite reference to subtract.
+    __device__ __forceinline__ float rebase(float nm, float c) {
+        const float ref = nm == -CUDART_INF_F ? 0.f : nm;
+        if (m == -CUDART_INF_F) {
+            l = w = 0.f;
+        } else {
+            const float d = fmaxf((m - nm) * c, -1e4f);   // finite: 2^d d is 0, not 0 * inf
+            const float f = ex2(d);
+            w = f * fmaf(d, l, w);
+            l *= f;
+        }
+        m = nm;
+        return ref;
+    }
+    __device__ __forceinline__ void add(float a, float ref, float c) {
+        float d = (a - ref) * c;
+        d = d < -1e4f ? -1e4f : d;          // -inf: 2^d d must be 0 (NaN stays NaN)
+        const float e = ex2(d);
+        l += e;
+        w = fmaf(e, d, w);
+    }
+};
+
+// KC best (value, column) pairs of one thread, sorted; equal values keep the
+// lower column when columns are offered in increasing order.
+template <int KC>
+struct ThreadTop {
+    float v[KC];
+    int id[KC];
+
+    // Only values above `floor` are kept.
+    __device__ __forceinline__ void init(float floor) {
+#pragma unroll
+        for (int i = 0; i < KC; ++i) { v[i] = floor; id[i] = -1; }
+    }
+    __device__ __forceinline__ void insert(float x, int col) {
+#pragma unroll
+        for (int i = KC - 1; i > 0; --i) {
+            const bool shift = x > v[i - 1];
+            const bool here = x > v[i];
+            id[i] = shift ? id[i - 1] : (here ? col : id[i]);
+            v[i] = shift ? v[i - 1] : (here ? x : v[i]);
+        }
+        if (x > v[0]) { v[0] = x; id[0] = col; }
+    }
+    __device__ __forceinline__ int count() const {
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < KC; ++i) n += id[i] >= 0 ? 1 : 0;
+        return n;
+    }
+};
+
+template <>
+struct ThreadTop<0> {};
+
+// a[i] for a run-time i without leaving the registers: five levels of selects.
+__device__ __forceinline__ float select32(const float (&a)[32], int i) {
+    float t[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) t[j] = (i & 16) ? a[j + 16] : a[j];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t[j] = (i & 8) ? t[j + 8] : t[j];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) t[j] = (i & 4) ? t[j + 4] : t[j];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) t[j] = (i & 2) ? t[j + 2] : t[j];
+    return (i & 1) ? t[1] : t[0];
+}
+
+// What a slice leaves for the merge.
+struct LpParts {
+    float4* stats;       // [n_parts][ld]  (m, l, w, entries as int bits)
+    float2* top;         // [n_parts][KC][ld]  (a, column as int bits), best first
+    uint32_t* floor;     // [ld] float_key of a value that KC columns of the row reach, or 0
+    int ld;              // rows of the chunk buffer
+};
+
+template <int KC>
+__device__ __forceinline__ void store_part(const LpParts& p, int part, int row,
+                                           const RunningStats& st, const ThreadTop<KC>& tt) {
+    int n = 0;
+    if constexpr (KC > 0) {
+        n = tt.count();
+#pragma unroll
+        for (int e = 0; e < KC; ++e)
+            if (e < n)
+                p.top[((size_t)part * KC + e) * p.ld + row] =
+                    make_float2(tt.v[e], __int_as_float(tt.id[e]));
+        if (n == KC) atomicMax(&p.floor[row], float_key(tt.v[KC - 1]));
+    }
+    p.stats[(size_t)part * p.ld + row] = make_float4(st.m, st.l, st.w, __int_as_float(n));
+}
+
+// A value just below the row's floor: columns below it cannot be among the
+// KC best, columns equal to it still can (by a lower id).
+__device__ __forceinline__ float row_floor(const LpParts& p, int row) {
+    const uint32_t k = __ldcg(&p.floor[row]);
+    return k == 0 ? -CUDART_INF_F : key_float(k - 1);
+}
+
+// ======================================================================
+// Epilogue of the tcgen05 sweep H W^T: one thread per row summarises its 256
+// columns.  Work per column is a multiply, a max, an exponential and three
+// adds; a column enters the candidate list only if it beats the row's floor,
+// which tiles publish as they finish, so after the first tiles few do (about
+// KC ln(V / KC) of V columns).  Floors only cut candidates that cannot be in
+// the result, so the result does not depend on the order of the tiles.
+// ======================================================================
+template <int KC>
+struct LogprobEpi {
+    struct Params {
+        float c;                     // |s| log2(e)
+        int neg;                     // s < 0: a = -(x W^T + b)
+        int64_t V;
+        int rows;
+        const __nv_bfloat16* bias;   // [V] or null
+        LpParts parts;
+    };
+
+    template <class Cfg>
+    static __device__ __forceinline__ void run(const Params& p, const TileCtx& t,
+                                               const AccRow& acc, Stager&) {
+        static_assert(Cfg::NSUB == 1, "one 256-column MMA per vocabulary tile");
+        const int m = t.row0 + t.row;
+        const int64_t n0 = t.col0;
+        const bool live = m < p.rows;
+        const int ncols = (int)((p.V - n0) < Cfg::BN ? (p.V - n0) : Cfg::BN);
+        const bool edge = p.bias != nullptr || ncols < Cfg::BN;   // a may be -inf
+        const float c = p.c;
+        RunningStats rs;
+        ThreadTop<KC> tt;
+        if constexpr (KC > 0) tt.init(live ? row_floor(p.parts, m) : CUDART_INF_F);
+        for_each_chunk<Cfg::NCHUNK>(acc, [&](const uint32_t (&rin)[32], int j) {
+            float a[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) a[i] = __uint_as_float(rin[i]);
+            if (p.bias != nullptr) {
+                float b[32];
+                load_bias32(p.bias, n0 + 32 * j, p.V, b);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) a[i] += b[i];
+            }
+            if (p.neg) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) a[i] = -a[i];
+            }
+            if (32 * j + 32 > ncols) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (32 * j + i >= ncols) a[i] = -CUDART_INF_F;
+            }
+            float cm0 = fmaxf(a[0], a[1]), cm1 = fmaxf(a[2], a[3]);
+#pragma unroll
+            for (int i = 4; i < 32; i += 4) {
+                cm0 = fmax3(cm0, a[i], a[i + 1]);
+                cm1 = fmax3(cm1, a[i + 2], a[i + 3]);
+            }
+            const float cm = fmaxf(cm0, cm1);
+            const float ref = rs.rebase(fmaxf(rs.m, cm), c);
+            float l0 = 0.f, l1 = 0.f, w0 = 0.f, w1 = 0.f;
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                float d0, d1;
+                add2(d0, d1, a[i], a[i + 1], -ref, -ref);
+                mul2(d0, d1, d0, d1, c, c);
+                if (edge) {
+                    d0 = d0 < -1e4f ? -1e4f : d0;
+                    d1 = d1 < -1e4f ? -1e4f : d1;
+                }
+                const float e0 = ex2(d0), e1 = ex2(d1);
+                add2(l0, l1, l0, l1, e0, e1);
+                fma2(w0, w1, e0, e1, d0, d1, w0, w1);
+            }
+            rs.l += l0 + l1;
+            rs.w += w0 + w1;
+            if constexpr (KC > 0) {
+                if (cm > tt.v[KC - 1]) {
+                    uint32_t mask = 0;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) mask |= (a[i] > tt.v[KC - 1] ? 1u : 0u) << i;
+                    while (mask != 0) {
+                        const int i = __ffs(mask) - 1;
+                        mask &= mask - 1;
+                        const float x = select32(a, i);
+                        if (x > tt.v[KC - 1]) tt.insert(x, (int)n0 + 32 * j + i);
+                    }
+                }
+            }
+        });
+        if (live) store_part<KC>(p.parts, (int)(n0 / Cfg::BN), m, rs, tt);
+    }
+};
+
+// The same over a 64-column tile of the fp32 CUDA-core GEMM.
+template <int KC>
+struct SimtLogprob {
+    float c;
+    int neg;
+    int64_t V;
+    int rows;
+    const float* bias;               // [V] fp32 or null
+    LpParts parts;
+    __device__ void operator()(float (*C)[kSimtTile + 1], int m0, int64_t n0, int nt) const {
+        const int r = threadIdx.x;
+        if (r >= kSimtTile || m0 + r >= rows) return;
+        const int ncols = (int)((V - n0) < kSimtTile ? (V - n0) : kSimtTile);
+        RunningStats rs;
+        ThreadTop<KC> tt;
+        if constexpr (KC > 0) tt.init(row_floor(parts, m0 + r));
+        float mx = -CUDART_INF_F;
+        for (int i = 0; i < ncols; ++i) {
+            float a = C[r][i] + (bias != nullptr ? bias[n0 + i] : 0.f);
+            if (neg) a = -a;
+            C[r][i] = a;
+            mx = fmaxf(mx, a);
+            if constexpr (KC > 0)
+                if (a > tt.v[KC - 1]) tt.insert(a, (int)n0 + i);
+        }
+        const float ref = rs.rebase(mx, c);
+        for (int i = 0; i < ncols; ++i) rs.add(C[r][i], ref, c);
+        store_part<KC>(parts, nt, m0 + r, rs, tt);
+    }
+};
+
+// ======================================================================
+// Candidate list of one row held across a warp: lane j < KC has the j-th best.
+// ======================================================================
+template <int KC>
+struct WarpTop {
+    float v = kNegInf;
+    int id = 0x7fffffff;
+
+    static __device__ __forceinline__ bool better(float xv, int xi, float yv, int yi) {
+        return xv > yv || (xv == yv && xi < yi);
+    }
+    // Every lane offers one (x, col); x = -inf (or NaN) offers nothing.
+    __device__ __forceinline__ void offer(float x, int col, int lane) {
+        float kv = __shfl_sync(0xffffffffu, v, KC - 1);
+        int ki = __shfl_sync(0xffffffffu, id, KC - 1);
+        uint32_t mask = __ballot_sync(0xffffffffu, x > -CUDART_INF_F && better(x, col, kv, ki));
+        while (mask != 0) {
+            const int src = __ffs(mask) - 1;
+            mask &= mask - 1;
+            const float xv = __shfl_sync(0xffffffffu, x, src);
+            const int xi = __shfl_sync(0xffffffffu, col, src);
+            const uint32_t ahead = __ballot_sync(0xffffffffu, lane < KC && better(v, id, xv, xi));
+            const int pos = __popc(ahead);         // the list is sorted: a prefix of lanes
+            const float pv = __shfl_up_sync(0xffffffffu, v, 1);
+            const int pi = __shfl_up_sync(0xffffffffu, id, 1);
+            if (lane > pos) { v = pv; id = pi; }
+            if (lane == pos) { v = xv; id = xi; }
+        }
+    }
+};
+
+// ---------------------------------------------------------------- exact dot products
+__device__ __forceinline__ double warp_sum(double x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// The weight of a head, whole (row-major, T = bf16 or fp32) or in 4 bits
+// (group > 0: two nibbles a byte, element 2i low, and a bf16 scale for each
+// group of a row).
+struct HeadWeight {
+    const void* W;
+    const __nv_bfloat16* scales;     // [V][groups]
+    int group;
+    int groups;
+};
+
+__device__ __forceinline__ int nibble(uint32_t w, int i) {
+    return ((int)(w << (28 - 4 * i))) >> 28;       // two's complement
+}
+
+// <x, W_v> by one warp.  Products of two bf16 (and of 4-bit values) are exact
+// in fp32; products of fp32 are taken in fp64; the sum is in fp64.
+template <class T>
+__device__ __forceinline__ double warp_dot(const T* __restrict__ x, const HeadWeight& hw,
+                                           int64_t v, int64_t D, int lane) {
+    double s = 0.0;
+    if constexpr (sizeof(T) == 2) {
+        const uint4* xq = reinterpret_cast<const uint4*>(x);
+        for (int64_t i = lane; i < D / 8; i += 32) {
+            const uint4 a = __ldg(xq + i);
+            const uint32_t au[4] = {a.x, a.y, a.z, a.w};
+            float f[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 t = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&au[k]));
+                f[2 * k] = t.x;
+                f[2 * k + 1] = t.y;
+            }
+            if (hw.group > 0) {
+                const uint32_t q =
+                    __ldg(reinterpret_cast<const uint32_t*>(hw.W) + (v * D) / 8 + i);
+                const float sc = __bfloat162float(hw.scales[v * hw.groups + (8 * i) / hw.group]);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) s += (double)(f[k] * ((float)nibble(q, k) * sc));
+            } else {
+                const uint4 b = __ldg(reinterpret_cast<const uint4*>(
+                                          static_cast<const __nv_bfloat16*>(hw.W) + v * D) + i);
+                const uint32_t bu[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 t =
+                        __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&bu[k]));
+                    s += (double)(f[2 * k] * t.x);
+                    s += (double)(f[2 * k + 1] * t.y);
+                }
+            }
+        }
+    } else {
+        const float* w = static_cast<const float*>(hw.W) + v * D;
+        for (int64_t i = lane; i < D; i += 32) s += (double)x[i] * (double)__ldg(w + i);
+    }
+    return warp_sum(s);
+}
+
+struct LpMergeParams {
+    LpParts parts;
+    int n_parts;
+    int rows;
+    int64_t D, V, ignore_index;
+    float s, c;
+    const void* H;                   // chunk's hidden states [rows, D]
+    HeadWeight hw;
+    const void* bias;                // [V] (type of H) or null
+    const int64_t* token;            // chunk's tokens or null
+    int k;
+    float* logprob;                  // chunk's outputs, each may be null
+    float* entropy;
+    float* lse;
+    int32_t* top_ids;                // [rows][k]
+    float* top_logprobs;             // [rows][k]
+    int32_t* n_err;                  // counts tokens outside [0, V), or null
+};
+
+constexpr int kLpMergeThreads = 128;
+
+// One block per row: the slices' statistics are combined in fp64, its warps
+// gather the KC best candidates, and every candidate (and the given token)
+// gets its dot product in fp64.
+template <int KC, class T>
+__global__ void __launch_bounds__(kLpMergeThreads) k_logprob_merge(const LpMergeParams p) {
+    constexpr int NW = kLpMergeThreads / 32;
+    const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ float sm_max[NW];
+    __shared__ double sm_l[NW], sm_w[NW];
+    __shared__ float sm_v[NW][32];
+    __shared__ int sm_id[NW][32];
+    __shared__ double sm_z[33];
+    __shared__ int sm_cand[33];
+
+    float mx = -CUDART_INF_F;
+    for (int k = tid; k < p.n_parts; k += kLpMergeThreads)
+        mx = fmaxf(mx, p.parts.stats[(size_t)k * p.parts.ld + row].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if (lane == 0) sm_max[warp] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NW; ++i) mx = fmaxf(mx, sm_max[i]);
+
+    double l = 0.0, w = 0.0;
+    WarpTop<KC == 0 ? 1 : KC> wt;
+    for (int k0 = 32 * warp; k0 < p.n_parts; k0 += kLpMergeThreads) {
+        const int k = k0 + lane;
+        float4 s = make_float4(-CUDART_INF_F, 0.f, 0.f, 0.f);
+        if (k < p.n_parts) s = p.parts.stats[(size_t)k * p.parts.ld + row];
+        if (s.x != -CUDART_INF_F || s.y != 0.f) {      // a slice with a logit (or a NaN)
+            const float d = fmaxf((s.x - mx) * p.c, -1e4f);
+            const double f = (double)exp2f(d);
+            l += f * s.y;
+            w += f * ((double)s.z + (double)d * s.y);
+        }
+        if constexpr (KC > 0) {
+            const int n = __float_as_int(s.w);
+            for (int e = 0; e < KC; ++e) {
+                float x = -CUDART_INF_F;
+                int id = 0x7fffffff;
+                if (e < n) {
+                    const float2 t = p.parts.top[((size_t)k * KC + e) * p.parts.ld + row];
+                    x = t.x;
+                    id = __float_as_int(t.y);
+                }
+                // lists are sorted: once no slice's e-th entry enters, none further does
+                const float kv = __shfl_sync(0xffffffffu, wt.v, KC - 1);
+                if (!__any_sync(0xffffffffu, x > -CUDART_INF_F && x >= kv)) break;
+                wt.offer(x, id, lane);
+            }
+        }
+    }
+    l = warp_sum(l);
+    w = warp_sum(w);
+    if (lane == 0) { sm_l[warp] = l; sm_w[warp] = w; }
+    if constexpr (KC > 0) { sm_v[warp][lane] = wt.v; sm_id[warp][lane] = wt.id; }
+    __syncthreads();
+    if constexpr (KC > 0) {
+        if (warp == 0) {
+            for (int i = 1; i < NW; ++i)
+                wt.offer(lane < KC ? sm_v[i][lane] : -CUDART_INF_F, sm_id[i][lane], lane);
+            sm_cand[lane] = lane < KC && wt.v > -CUDART_INF_F ? wt.id : -1;
+        }
+    }
+    int64_t y = -1;
+    if (p.token != nullptr) {
+        const int64_t t = p.token[row];
+        if (t != p.ignore_index) {
+            if (t >= 0 && t < p.V) y = t;
+            else if (tid == 0 && p.n_err != nullptr) atomicAdd(p.n_err, 1);
+        }
+    }
+    if (tid == 0) sm_cand[32] = (int)y;
+    __syncthreads();
+    const T* x = static_cast<const T*>(p.H) + (int64_t)row * p.D;
+    for (int i = warp; i <= KC; i += NW) {             // KC candidates, then the given token
+        const int slot = i == KC ? 32 : i;
+        const int v = sm_cand[slot];
+        if (v < 0) continue;                           // the same for the whole warp
+        double z = warp_dot<T>(x, p.hw, v, p.D, lane);
+        if (p.bias != nullptr) {
+            if constexpr (sizeof(T) == 2)
+                z += (double)__bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[v]);
+            else
+                z += (double)static_cast<const float*>(p.bias)[v];
+        }
+        if (lane == 0) sm_z[slot] = (double)p.s * z;
+    }
+    __syncthreads();
+    if (warp != 0) return;
+    l = sm_l[0];
+    w = sm_w[0];
+#pragma unroll
+    for (int i = 1; i < NW; ++i) { l += sm_l[i]; w += sm_w[i]; }
+    // every logit -inf: lse = -inf, no information in the row
+    const bool none = mx == -CUDART_INF_F && l == 0.0;
+    const double lnl = none ? 0.0 : log(l);
+    // |s| mx, the largest logit, in fp64
+    const double lse = none ? -CUDART_INF : (double)fabsf(p.s) * (double)mx + lnl;
+    if (lane == 0) {
+        if (p.lse != nullptr) p.lse[row] = (float)lse;
+        if (p.entropy != nullptr)
+            p.entropy[row] = none ? 0.f : (float)(lnl - 0.69314718055994530942 * (w / l));
+        if (p.logprob != nullptr)
+            p.logprob[row] = y < 0 ? 0.f : (none ? -CUDART_INF_F : (float)(sm_z[32] - lse));
+    }
+    if constexpr (KC > 0) {
+        const int id = sm_cand[lane];
+        const double z = id >= 0 ? sm_z[lane] : -CUDART_INF;
+        int rank = 0;
+        for (int j = 0; j < KC; ++j) {
+            const double zj = __shfl_sync(0xffffffffu, z, j);
+            const int ij = __shfl_sync(0xffffffffu, id, j);
+            if (ij >= 0 && (zj > z || (zj == z && ij < id))) ++rank;
+        }
+        const int found = __popc(__ballot_sync(0xffffffffu, id >= 0));
+        if (id >= 0 && rank < p.k) {
+            p.top_ids[(size_t)row * p.k + rank] = id;
+            p.top_logprobs[(size_t)row * p.k + rank] = (float)(z - lse);
+        }
+        if (lane >= found && lane < p.k) {             // fewer logits above -inf than asked for
+            p.top_ids[(size_t)row * p.k + lane] = -1;
+            p.top_logprobs[(size_t)row * p.k + lane] = -CUDART_INF_F;
+        }
+    }
+}
+
+// ======================================================================
+// Gradient.  For upstream a = d/d logprob (0 where the token is ignored) and
+// e = d/d entropy:
+//   G_v = s ( p_v (-(a + e entropy) - e log p_v) + a [v = y] ).
+// With q = acc c' - lse log2(e) = log2 p_v:  G_v = 2^q (kap - ee q) + ta [v = y].
+// ======================================================================
+struct LpCoef {
+    float* lse2;         // [chunk]
+    float* kap;
+    float* ee;
+    float* ta;
+    int32_t* y;          // validated token or -1
+};
+
+__global__ void k_logprob_coef(const int64_t* __restrict__ token, const float* __restrict__ lse,
+                               const float* __restrict__ entropy, const float* __restrict__ dlp,
+                               const float* __restrict__ dent, int rows, int64_t V,
+                               int64_t ignore_index, float s, LpCoef o, int32_t* n_err) {
+    const int i = blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= rows) return;
+    int64_t y = token != nullptr ? token[i] : ignore_index;
+    if (y != ignore_index && (y < 0 || y >= V)) {
+        if (n_err != nullptr) atomicAdd(n_err, 1);
+        y = ignore_index;
+    }
+    const bool has = y != ignore_index;
+    const float L = lse[i];
+    const bool none = L == -CUDART_INF_F;          // every logit -inf: nothing to move
+    const float a = has && dlp != nullptr && !none ? dlp[i] : 0.f;
+    const float e = dent != nullptr && !none ? dent[i] : 0.f;
+    o.lse2[i] = none ? 0.f : L * 1.4426950408889634f;
+    o.kap[i] = e == 0.f ? -s * a : -s * fmaf(e, entropy[i], a);
+    o.ee[i] = s * e * 0.69314718055994530942f;
+    o.ta[i] = s * a;
+    o.y[i] = has ? (int32_t)y : -1;
+}
+
+// One element: q = log2 p.  A row without upstream gradient is exactly 0.
+__device__ __forceinline__ float lp_grad(float q, float kap, float ee) {
+    q = q < -1e4f ? -1e4f : q;                     // a logit of -inf: p = 0, not 0 * inf
+    return ex2(q) * fmaf(-ee, q, kap);
+}
+
+struct LogprobGEpi {
+    struct Params {
+        CUtensorMap gmap;            // G [rows, V] bf16, box 64 x 32, 128B swizzle
+        float c;                     // s log2(e)
+        int64_t V;
+        int rows;
+        LpCoef k;
+        const __nv_bfloat16* bias;   // [V] or null
+    };
+
+    // G is rounded once to bf16, the operand type of the dH and dW products.
+    template <class Cfg>
+    static __device__ __forceinline__ void run(const Params& p, const TileCtx& t,
+                                               const AccRow& acc, Stager& st) {
+        static_assert(Cfg::NSUB == 1, "one 256-column MMA per vocabulary tile");
+        const int64_t n0 = t.col0;
+        const int m = t.row0 + t.row;
+        float L2 = 0.f, kap = 0.f, ee = 0.f, ta = 0.f;
+        int yrel = -1;
+        if (m < p.rows) {
+            L2 = p.k.lse2[m];
+            kap = p.k.kap[m];
+            ee = p.k.ee[m];
+            ta = p.k.ta[m];
+            const int y = p.k.y[m];
+            if (y >= n0 && y < n0 + Cfg::BN) yrel = (int)(y - n0);
+        }
+        const bool dead = kap == 0.f && ee == 0.f && ta == 0.f;
+        const int ncols = (int)((p.V - n0) < Cfg::BN ? (p.V - n0) : Cfg::BN);
+        const float c = p.c;
+        for_each_chunk<Cfg::NCHUNK>(acc, [&](const uint32_t (&r)[32], int j) {
+            float g[32];
+            if (p.bias != nullptr) {
+                float b[32];
+                load_bias32(p.bias, n0 + 32 * j, p.V, b);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    g[i] = lp_grad(fmaf(__uint_as_float(r[i]) + b[i], c, -L2), kap, ee);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    float q0, q1, k0, k1;
+                    fma2(q0, q1, __uint_as_float(r[i]), __uint_as_float(r[i + 1]), c, c, -L2, -L2);
+                    fma2(k0, k1, q0, q1, -ee, -ee, kap, kap);
+                    mul2(g[i], g[i + 1], k0, k1, ex2(q0), ex2(q1));
+                }
+            }
+            if ((unsigned)(yrel - 32 * j) < 32u) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (i == yrel - 32 * j) g[i] += ta;
+            }
+            if (dead) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) g[i] = 0.f;
+            }
+            if (32 * j + 32 > ncols) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (32 * j + i >= ncols) g[i] = 0.f;
+            }
+            if ((j & 1) == 0) st.acquire();
+            stage_bf16_half(st, j, g);
+            if (j & 1) st.flush(&p.gmap, (int)(n0 + 32 * (j - 1)), t.row0 + 32 * t.q, false);
+        });
+    }
+};
+
+struct SimtLogprobG {
+    float c;
+    int64_t V, ldg;
+    int rows;
+    LpCoef k;
+    float* G;
+    const float* bias;               // [V] fp32 or null
+    __device__ void operator()(float (*C)[kSimtTile + 1], int m0, int64_t n0, int) const {
+        for (int idx = threadIdx.x; idx < kSimtTile * kSimtTile; idx += blockDim.x) {
+            const int r = idx / kSimtTile, i = idx % kSimtTile;
+            const int m = m0 + r;
+            const int64_t v = n0 + i;
+            if (m >= rows || v >= ldg) continue;
+            float g = 0.f;
+            const float kap = k.kap[m], ee = k.ee[m], ta = k.ta[m];
+            if (v < V && !(kap == 0.f && ee == 0.f && ta == 0.f)) {
+                const float a = C[r][i] + (bias != nullptr ? bias[v] : 0.f);
+                g = lp_grad(fmaf(a, c, -k.lse2[m]), kap, ee);
+                if (v == k.y[m]) g += ta;
+            }
+            G[(size_t)m * ldg + v] = g;
+        }
+    }
+};
+
+}  // namespace fldce

@@ -1,0 +1,388 @@
+// logprob_host.cuh -- host side of the token log-probabilities and of the
+// 4-bit head weight (fldce_logprob*, fldce_w4_*).  Included by fldce_api.cu,
+// whose launch helpers it uses.
+//
+// Forward, per chunk of tokens: a sweep leaves every vocabulary slice's
+// statistics and candidates, k_logprob_merge joins them.  Backward, per chunk:
+// k_logprob_coef turns the upstream gradients into row coefficients, one
+// sweep recomputes the logits into G, and the training path's dH and dW
+// products follow.
+#pragma once
+
+namespace {
+
+// Partial statistics of one forward chunk: at most this much workspace.
+constexpr size_t kLpBudget = size_t(512) << 20;
+constexpr int64_t kW4PassRows = 256;            // tokens of a forward chunk on a 4-bit weight
+
+struct LpLayout {
+    size_t cnt, stats, top, floor, logits, total;
+    int64_t C;                // tokens per chunk
+    int64_t n_parts;
+    int kc;
+};
+
+LpLayout lp_layout(const fldce_plan* p, int64_t N, int top_k, bool w4) {
+    LpLayout L{};
+    L.kc = candidates_for(top_k);
+    L.n_parts = w4 ? cdiv(p->cfg.V, kLogitPart) : p->n_vt;
+    const size_t per_row = (size_t)L.n_parts * (16 + 8 * (size_t)L.kc);
+    int64_t C = std::max<int64_t>(256, (int64_t)(kLpBudget / per_row) / 256 * 256);
+    if (w4) C = kW4PassRows;
+    L.C = std::max<int64_t>(1, std::min(C, N));
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = off;
+        off = round_up(off + bytes, kAlign);
+        return o;
+    };
+    L.cnt = take(sizeof(Counters));
+    L.stats = take((size_t)L.n_parts * L.C * 16);
+    L.top = take((size_t)L.n_parts * L.C * L.kc * 8);
+    L.floor = take((size_t)L.C * 4);
+    L.logits = take(w4 ? (size_t)kW4Tokens * p->cfg.V * 4 : 0);
+    L.total = off;
+    return L;
+}
+
+// Shapes every 4-bit weight has to have.
+int check_w4(const void* packed, const void* scales, int group, int64_t V, int64_t D) {
+    if (V <= 0 || D <= 0) return FLDCE_ERR_INVALID_ARG;
+    if (packed == nullptr || scales == nullptr) return FLDCE_ERR_INVALID_ARG;
+    if (D % 32 != 0 || (group != 32 && group != 64 && group != 128)) return FLDCE_ERR_UNSUPPORTED;
+    if (V > (int64_t(1) << 31) - 1 || D > (int64_t(1) << 31) - 1) return FLDCE_ERR_UNSUPPORTED;
+    if (!aligned16(packed) || !aligned_to(scales, 2)) return FLDCE_ERR_ALIGN;
+    return FLDCE_OK;
+}
+
+HeadWeight w4_weight(const void* packed, const void* scales, int group, int64_t D) {
+    return HeadWeight{packed, static_cast<const __nv_bfloat16*>(scales), group,
+                      (int)cdiv(D, group)};
+}
+
+template <class OutT>
+cudaError_t launch_w4_rows(const __nv_bfloat16* x, int n_tok, const HeadWeight& hw,
+                           const __nv_bfloat16* bias, int64_t V, int64_t D, OutT* out, int64_t ldo,
+                           int sms, cudaStream_t st) {
+    const int blocks = (int)std::min<int64_t>(cdiv(V, 8), 8 * (int64_t)sms);
+    k_w4_rows<OutT><<<blocks, 256, 0, st>>>(x, n_tok, hw, bias, V, D, out, ldo);
+    return cudaGetLastError();
+}
+
+template <int KC>
+int lp_forward(fldce_plan* h, const fldce_logprob_call& call, const LpLayout& L,
+               const DeviceInfo& dev) {
+    const fldce_config& cfg = h->cfg;
+    const int64_t D = cfg.D, V = cfg.V, N = call.N;
+    const bool bf16 = cfg.dtype == FLDCE_BF16, w4 = call.w4 != nullptr;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(call.stream);
+    uint8_t* ws = static_cast<uint8_t*>(call.workspace);
+    Counters* cnt = reinterpret_cast<Counters*>(ws + L.cnt);
+    LpParts parts{reinterpret_cast<float4*>(ws + L.stats), reinterpret_cast<float2*>(ws + L.top),
+                  reinterpret_cast<uint32_t*>(ws + L.floor), (int)L.C};
+    const float c = fabsf(cfg.logit_scale) * 1.4426950408889634f;
+    const int neg = cfg.logit_scale < 0.f ? 1 : 0;
+    HeadWeight hw{call.W, nullptr, 0, 0};
+    if (w4) hw = w4_weight(call.w4, call.w4_scales, call.w4_group, D);
+    CUtensorMap mW;
+    if (bf16 && !w4 && !make_map(&mW, call.W, D, V, D, 64, 128)) return FLDCE_ERR_CUDA;
+    for (int64_t r0 = 0; r0 < N; r0 += L.C) {
+        const int rows = (int)std::min<int64_t>(L.C, N - r0);
+        const uint8_t* Hc = static_cast<const uint8_t*>(call.H) + (size_t)r0 * D * h->elt;
+        if (KC > 0) FLDCE_CUDA(cudaMemsetAsync(parts.floor, 0, (size_t)rows * 4, st));
+        prof_mark(h, PK_GAP, st);
+        if (w4) {
+            const __nv_bfloat16* x = reinterpret_cast<const __nv_bfloat16*>(Hc);
+            float* logits = reinterpret_cast<float*>(ws + L.logits);
+            for (int t0 = 0; t0 < rows; t0 += kW4Tokens) {
+                const int nt = std::min(kW4Tokens, rows - t0);
+                FLDCE_CUDA(launch_w4_rows<float>(x + (int64_t)t0 * D, nt, hw,
+                                                 static_cast<const __nv_bfloat16*>(call.bias), V,
+                                                 D, logits, V, dev.sms, st));
+                k_logit_parts<KC><<<(unsigned)cdiv(L.n_parts * nt, 4), 128, 0, st>>>(
+                    logits, V, nt, t0, V, c, neg, parts, (int)L.n_parts);
+                FLDCE_CUDA(cudaGetLastError());
+            }
+        } else if (bf16) {
+            CUtensorMap mH;
+            if (!make_map(&mH, Hc, D, rows, D, 64, 128)) return FLDCE_ERR_CUDA;
+            typename LogprobEpi<KC>::Params ep{
+                c, neg, V, rows, static_cast<const __nv_bfloat16*>(call.bias), parts};
+            const Walk walk{0, 1, walk_group(cdiv(rows, CfgKK::PAIR_M),
+                                             (size_t)CfgKK::PAIR_M * D * 2, kL2BudgetSweep)};
+            FLDCE_CUDA((launch_gemm<CfgKK, LogprobEpi<KC>>(mH, mW, rows, V, D, walk, ep,
+                                                           &cnt->dev_err, dev.sms, st)));
+        } else {
+            SimtLogprob<KC> e{c, neg, V, rows, static_cast<const float*>(call.bias), parts};
+            FLDCE_CUDA(launch_simt(reinterpret_cast<const float*>(Hc), D, 1,
+                                   static_cast<const float*>(call.W), D, 1, rows, V, (int)D, e,
+                                   st));
+        }
+        prof_mark(h, PK_LSE, st);
+        LpMergeParams mp{};
+        mp.parts = parts;
+        mp.n_parts = (int)L.n_parts;
+        mp.rows = rows;
+        mp.D = D;
+        mp.V = V;
+        mp.ignore_index = cfg.ignore_index;
+        mp.s = cfg.logit_scale;
+        mp.c = c;
+        mp.H = Hc;
+        mp.hw = hw;
+        mp.bias = call.bias;
+        mp.token = call.token != nullptr ? call.token + r0 : nullptr;
+        mp.k = call.top_k;
+        mp.logprob = call.logprob != nullptr ? call.logprob + r0 : nullptr;
+        mp.entropy = call.entropy != nullptr ? call.entropy + r0 : nullptr;
+        mp.lse = call.lse != nullptr ? call.lse + r0 : nullptr;
+        mp.top_ids = KC > 0 ? call.top_ids + r0 * call.top_k : nullptr;
+        mp.top_logprobs = KC > 0 ? call.top_logprobs + r0 * call.top_k : nullptr;
+        mp.n_err = call.err_count;
+        if (bf16)
+            k_logprob_merge<KC, __nv_bfloat16><<<rows, kLpMergeThreads, 0, st>>>(mp);
+        else
+            k_logprob_merge<KC, float><<<rows, kLpMergeThreads, 0, st>>>(mp);
+        FLDCE_CUDA(cudaGetLastError());
+        prof_mark(h, PK_MERGE, st);
+    }
+    // the device error bits of the sweeps
+    if (call.err_count != nullptr)
+        FLDCE_CUDA(cudaMemcpyAsync(call.err_count + 1, &cnt->dev_err, 4, cudaMemcpyDeviceToDevice,
+                                   st));
+    return FLDCE_OK;
+}
+
+// What the log-probability entry points accept of a plan.
+int check_lp_plan(const fldce_plan* h) {
+    if (h->sharded || (h->cfg.flags & (FLDCE_FLAG_SKIP_IGNORED | FLDCE_FLAG_FUSED_DH)) != 0)
+        return FLDCE_ERR_UNSUPPORTED;
+    return FLDCE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fldce_logprob_workspace_size(fldce_handle h, int64_t N, int32_t top_k, size_t* bytes) {
+    if (h == nullptr || bytes == nullptr || N < 0 || N > h->cfg.max_N) return FLDCE_ERR_INVALID_ARG;
+    if (top_k < 0 || top_k > FLDCE_MAX_TOP_K || top_k > h->cfg.V) return FLDCE_ERR_INVALID_ARG;
+    if (int e = check_lp_plan(h)) return e;
+    *bytes = std::max(lp_layout(h, N, top_k, false).total, lp_layout(h, N, top_k, true).total);
+    return FLDCE_OK;
+}
+
+int fldce_logprob(fldce_handle h, const fldce_logprob_call* cp) {
+    if (h == nullptr || cp == nullptr) return FLDCE_ERR_INVALID_ARG;
+    const fldce_logprob_call& c = *cp;
+    if (int e = check_lp_plan(h)) return e;
+    const bool w4 = c.w4 != nullptr;
+    if (c.N < 0 || c.N > h->cfg.max_N || c.top_k < 0 || c.top_k > FLDCE_MAX_TOP_K ||
+        c.top_k > h->cfg.V)
+        return FLDCE_ERR_INVALID_ARG;
+    if ((c.W != nullptr) == w4) return FLDCE_ERR_INVALID_ARG;
+    if (c.N > 0 && c.H == nullptr) return FLDCE_ERR_INVALID_ARG;
+    if (c.logprob != nullptr && c.token == nullptr) return FLDCE_ERR_INVALID_ARG;
+    if (c.N > 0 && c.top_k > 0 && (c.top_ids == nullptr || c.top_logprobs == nullptr))
+        return FLDCE_ERR_INVALID_ARG;
+    if (w4) {
+        if (h->cfg.dtype != FLDCE_BF16) return FLDCE_ERR_UNSUPPORTED;
+        if (int e = check_w4(c.w4, c.w4_scales, c.w4_group, h->cfg.V, h->cfg.D)) return e;
+    }
+    if (c.workspace == nullptr || !aligned_to(c.workspace, kAlign)) return FLDCE_ERR_WORKSPACE;
+    if (!aligned16(c.H) || !aligned16(c.W) || !aligned16(c.bias)) return FLDCE_ERR_ALIGN;
+    if (!aligned_to(c.token, 8) || !aligned_to(c.logprob, 4) || !aligned_to(c.entropy, 4) ||
+        !aligned_to(c.lse, 4) || !aligned_to(c.top_ids, 4) || !aligned_to(c.top_logprobs, 4) ||
+        !aligned_to(c.err_count, 4))
+        return FLDCE_ERR_ALIGN;
+    const LpLayout L = lp_layout(h, c.N, c.top_k, w4);
+    if (c.workspace_bytes < L.total) return FLDCE_ERR_WORKSPACE;
+    DeviceInfo dev;
+    if (int s = check_device(&dev)) return s;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(c.stream);
+    if (c.err_count != nullptr) {
+        Counters* cnt = reinterpret_cast<Counters*>(static_cast<uint8_t*>(c.workspace) + L.cnt);
+        FLDCE_CUDA(cudaMemsetAsync(c.err_count, 0, 8, st));
+        FLDCE_CUDA(cudaMemsetAsync(cnt, 0, sizeof(Counters), st));
+    }
+    if (c.N == 0) return FLDCE_OK;
+    switch (L.kc) {
+        case 0: return lp_forward<0>(h, c, L, dev);
+        case candidates_for(1): return lp_forward<candidates_for(1)>(h, c, L, dev);
+        case candidates_for(5): return lp_forward<candidates_for(5)>(h, c, L, dev);
+        default: return lp_forward<candidates_for(FLDCE_MAX_TOP_K)>(h, c, L, dev);
+    }
+}
+
+int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
+    if (h == nullptr || cp == nullptr) return FLDCE_ERR_INVALID_ARG;
+    const fldce_logprob_grad_call& c = *cp;
+    if (int e = check_lp_plan(h)) return e;
+    const fldce_config& cfg = h->cfg;
+    const int64_t N = c.N, D = cfg.D, V = cfg.V;
+    if (N < 0 || N > cfg.max_N) return FLDCE_ERR_INVALID_ARG;
+    if (c.dH == nullptr && c.dW == nullptr && c.db == nullptr && N > 0) return FLDCE_ERR_INVALID_ARG;
+    if (N > 0 && (c.H == nullptr || c.W == nullptr || c.lse == nullptr)) return FLDCE_ERR_INVALID_ARG;
+    if (N > 0 && c.dlogprob != nullptr && c.token == nullptr) return FLDCE_ERR_INVALID_ARG;
+    if (N > 0 && c.dentropy != nullptr && c.entropy == nullptr) return FLDCE_ERR_INVALID_ARG;
+    if (c.db != nullptr && c.bias == nullptr) return FLDCE_ERR_INVALID_ARG;
+    if (c.workspace == nullptr || !aligned_to(c.workspace, kAlign)) return FLDCE_ERR_WORKSPACE;
+    if (!aligned16(c.H) || !aligned16(c.W) || !aligned16(c.bias) || !aligned16(c.dH) ||
+        !aligned16(c.dW) || !aligned16(c.db))
+        return FLDCE_ERR_ALIGN;
+    if (!aligned_to(c.token, 8) || !aligned_to(c.lse, 4) || !aligned_to(c.entropy, 4) ||
+        !aligned_to(c.dlogprob, 4) || !aligned_to(c.dentropy, 4) || !aligned_to(c.err_count, 4))
+        return FLDCE_ERR_ALIGN;
+    const Layout L = make_layout(h, N);
+    if (c.workspace_bytes < L.total) return FLDCE_ERR_WORKSPACE;
+    DeviceInfo dev;
+    if (int s = check_device(&dev)) return s;
+
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(c.stream);
+    uint8_t* ws = static_cast<uint8_t*>(c.workspace);
+    Counters* cnt = reinterpret_cast<Counters*>(ws + L.cnt);
+    const bool bf16 = cfg.dtype == FLDCE_BF16, accum = dw_accumulate(h);
+    const size_t dw_elt = dw_out_fp32(h) ? 4 : h->elt;
+    const float c2 = cfg.logit_scale * 1.4426950408889634f;
+    if (c.err_count != nullptr) {
+        FLDCE_CUDA(cudaMemsetAsync(c.err_count, 0, 8, st));
+        FLDCE_CUDA(cudaMemsetAsync(cnt, 0, sizeof(Counters), st));
+    }
+    if (N == 0) {
+        if (!accum && c.dW != nullptr)
+            FLDCE_CUDA(cudaMemsetAsync(c.dW, 0, (size_t)V * D * dw_elt, st));
+        if (!accum && c.db != nullptr) FLDCE_CUDA(cudaMemsetAsync(c.db, 0, (size_t)V * dw_elt, st));
+        return FLDCE_OK;
+    }
+    LpCoef k{reinterpret_cast<float*>(ws + L.row_lse2), reinterpret_cast<float*>(ws + L.row_gcoef),
+             reinterpret_cast<float*>(ws + L.zy), reinterpret_cast<float*>(ws + L.loss_tok),
+             reinterpret_cast<int32_t*>(ws + L.row_y)};
+    float* db_part = reinterpret_cast<float*>(ws + L.db_part);
+    float* db_acc = reinterpret_cast<float*>(ws + L.db_acc);
+    CUtensorMap mW_k, mW_mn;
+    if (bf16 && (!make_map(&mW_k, c.W, D, V, D, 64, 128) || !make_map(&mW_mn, c.W, D, V, D, 64, 64)))
+        return FLDCE_ERR_CUDA;
+    prof_mark(h, PK_GAP, st);
+    for (int64_t ci = 0; ci < L.nchunks; ++ci) {
+        const int64_t r0 = ci * h->chunk;
+        const int rows = (int)std::min<int64_t>(h->chunk, N - r0);
+        k_logprob_coef<<<(unsigned)cdiv(rows, 256), 256, 0, st>>>(
+            c.token != nullptr ? c.token + r0 : nullptr, c.lse + r0,
+            c.entropy != nullptr ? c.entropy + r0 : nullptr,
+            c.dlogprob != nullptr ? c.dlogprob + r0 : nullptr,
+            c.dentropy != nullptr ? c.dentropy + r0 : nullptr, rows, V, cfg.ignore_index,
+            cfg.logit_scale, k, c.err_count);
+        FLDCE_CUDA(cudaGetLastError());
+        prof_mark(h, PK_MERGE, st);
+        const uint8_t* Hc = static_cast<const uint8_t*>(c.H) + (size_t)r0 * D * h->elt;
+        void* G = ws + L.G;
+        if (bf16) {
+            CUtensorMap mH_k, mH_mn, mG_k, mG_mn;
+            LogprobGEpi::Params gp;
+            if (!make_store_map(&gp.gmap, G, V, rows, h->Vpad, 2) ||
+                !make_map(&mH_k, Hc, D, rows, D, 64, 128) ||
+                !make_map(&mH_mn, Hc, D, rows, D, 64, 64) ||
+                !make_map(&mG_k, G, V, rows, h->Vpad, 64, 128) ||
+                !make_map(&mG_mn, G, V, rows, h->Vpad, 64, 64))
+                return FLDCE_ERR_CUDA;
+            gp.c = c2;
+            gp.V = V;
+            gp.rows = rows;
+            gp.k = k;
+            gp.bias = static_cast<const __nv_bfloat16*>(c.bias);
+            const Walk walk{0, 1, walk_group(cdiv(rows, CfgKK::PAIR_M),
+                                             (size_t)CfgKK::PAIR_M * D * 2, kL2BudgetSweep)};
+            FLDCE_CUDA((launch_gemm<CfgKK, LogprobGEpi>(mH_k, mW_k, rows, V, D, walk, gp,
+                                                        &cnt->dev_err, dev.sms, st)));
+            prof_mark(h, PK_G, st);
+            const GradGemm gg{h, &L, ws, cnt, &dev, st, rows, r0, DynRows()};
+            if (c.dH != nullptr)
+                if (int e = gg.dh(mG_k, mW_mn, c.dH)) return e;
+            if (c.dW != nullptr)
+                if (int e = gg.dw(mG_mn, mH_mn, c.dW, ci)) return e;
+        } else {
+            const float* Hf = reinterpret_cast<const float*>(Hc);
+            const float* Wf = static_cast<const float*>(c.W);
+            float* Gf = static_cast<float*>(G);
+            SimtLogprobG ge{c2, V, h->Vpad, rows, k, Gf, static_cast<const float*>(c.bias)};
+            FLDCE_CUDA(launch_simt(Hf, D, 1, Wf, D, 1, rows, V, (int)D, ge, st));
+            prof_mark(h, PK_G, st);
+            if (c.dH != nullptr) {
+                SimtStore hs{rows, D, D, static_cast<float*>(c.dH) + r0 * D, nullptr, 0};
+                FLDCE_CUDA(launch_simt(Gf, h->Vpad, 1, Wf, 1, D, rows, D, (int)V, hs, st));
+                prof_mark(h, PK_DH, st);
+            }
+            if (c.dW != nullptr) {
+                float* dw = static_cast<float*>(c.dW);
+                const int mode = accum ? 2 : (L.nchunks == 1 ? 0 : (ci == 0 ? 1 : 2));
+                SimtStore wsd{(int)V, D, D, dw, dw, mode};
+                FLDCE_CUDA(launch_simt(Gf, 1, h->Vpad, Hf, 1, D, (int)V, D, rows, wsd, st));
+                prof_mark(h, PK_DW, st);
+            }
+        }
+        if (c.db != nullptr) {
+            FLDCE_CUDA(launch_colsum(G, bf16, h->Vpad, rows, V, db_part, db_acc, ci > 0, st));
+            if (ci + 1 == L.nchunks) {
+                k_cast_out<<<(unsigned)cdiv(V, 256), 256, 0, st>>>(
+                    db_acc, c.db, V, dw_out_fp32(h) ? 0 : 1, accum ? 1 : 0);
+                FLDCE_CUDA(cudaGetLastError());
+            }
+            prof_mark(h, PK_DB, st);
+        }
+    }
+    if (c.err_count != nullptr)
+        FLDCE_CUDA(cudaMemcpyAsync(c.err_count + 1, &cnt->dev_err, 4, cudaMemcpyDeviceToDevice,
+                                   st));
+    return FLDCE_OK;
+}
+
+int fldce_w4_quantize(const void* W, int32_t dtype, int64_t V, int64_t D, int32_t group,
+                      void* packed, void* scales, void* stream) {
+    if (W == nullptr) return FLDCE_ERR_INVALID_ARG;
+    if (dtype != FLDCE_BF16 && dtype != FLDCE_FP32) return FLDCE_ERR_UNSUPPORTED;
+    if (int e = check_w4(packed, scales, group, V, D)) return e;
+    if (!aligned16(W)) return FLDCE_ERR_ALIGN;
+    DeviceInfo dev;
+    if (int s = check_device(&dev)) return s;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const int blocks = (int)std::min<int64_t>(cdiv(V * cdiv(D, group), 8), 16 * (int64_t)dev.sms);
+    uint8_t* q = static_cast<uint8_t*>(packed);
+    __nv_bfloat16* sc = static_cast<__nv_bfloat16*>(scales);
+    if (dtype == FLDCE_BF16)
+        k_w4_quantize<<<blocks, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(W), V, D, group, q,
+                                              sc);
+    else
+        k_w4_quantize<<<blocks, 256, 0, st>>>(static_cast<const float*>(W), V, D, group, q, sc);
+    return cudaGetLastError() == cudaSuccess ? FLDCE_OK : FLDCE_ERR_CUDA;
+}
+
+int fldce_w4_linear(const void* x, int64_t N, const void* packed, const void* scales, int32_t group,
+                    const void* bias, int64_t V, int64_t D, void* out, int32_t out_dtype,
+                    void* stream) {
+    if (N < 0 || N > (int64_t(1) << 31) - 1) return FLDCE_ERR_INVALID_ARG;
+    if (out_dtype != FLDCE_BF16 && out_dtype != FLDCE_FP32) return FLDCE_ERR_UNSUPPORTED;
+    if (int e = check_w4(packed, scales, group, V, D)) return e;
+    if (N == 0) return FLDCE_OK;
+    if (x == nullptr || out == nullptr) return FLDCE_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned_to(bias, 2) ||
+        !aligned_to(out, out_dtype == FLDCE_BF16 ? 2 : 4))
+        return FLDCE_ERR_ALIGN;
+    DeviceInfo dev;
+    if (int s = check_device(&dev)) return s;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const HeadWeight hw = w4_weight(packed, scales, group, D);
+    const __nv_bfloat16* xb = static_cast<const __nv_bfloat16*>(x);
+    const __nv_bfloat16* b = static_cast<const __nv_bfloat16*>(bias);
+    for (int64_t t0 = 0; t0 < N; t0 += kW4Tokens) {
+        const int nt = (int)std::min<int64_t>(kW4Tokens, N - t0);
+        if (out_dtype == FLDCE_BF16)
+            FLDCE_CUDA(launch_w4_rows(xb + t0 * D, nt, hw, b, V, D,
+                                      static_cast<__nv_bfloat16*>(out) + t0 * V, V, dev.sms, st));
+        else
+            FLDCE_CUDA(launch_w4_rows(xb + t0 * D, nt, hw, b, V, D,
+                                      static_cast<float*>(out) + t0 * V, V, dev.sms, st));
+    }
+    return FLDCE_OK;
+}
+
+}  // extern "C"

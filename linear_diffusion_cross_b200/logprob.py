@@ -1,0 +1,188 @@
+"""Log-probabilities of given tokens, entropy and the best alternatives from
+hidden states and the head's weight, without the logits in memory.
+
+``fused_linear_logprobs(x, token, weight, ...)`` is what scoring, decoding and
+policy-gradient training ask of the head that ``FusedLinearDiffusionCrossEntropyLoss``
+trains.  ``logprob`` and ``entropy`` are differentiable in x, weight and bias;
+the backward recomputes the logits in one sweep (``fldce_logprob_bwd``).  The
+weight may be a ``W4Weight`` (forward only).
+
+Workspaces come from PyTorch's allocator per call, on the call's own stream:
+calls on several streams, and captured graphs, share none.
+"""
+from __future__ import annotations
+
+from typing import NamedTuple, Optional, Union
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import binding as B
+from .module import _dtype_code
+from .w4 import W4Weight, check_w4_input, dense, on_device_of
+
+_MAX_N = (1 << 31) - 1
+_HANDLES = {}
+
+
+def _handle(dtype: torch.dtype, D: int, V: int, logit_scale: float, ignore_index: int,
+            chunk_n: int) -> int:
+    """A plan's host state (no device memory), one per configuration."""
+    key = (dtype, D, V, logit_scale, ignore_index, chunk_n)
+    h = _HANDLES.get(key)
+    if h is None:
+        h, _ = B.fldce_create(_dtype_code(dtype), D, V, _MAX_N, chunk_N=chunk_n,
+                              logit_scale=logit_scale, ignore_index=ignore_index)
+        h = _HANDLES.setdefault(key, h)
+    return h
+
+
+class LinearLogProbs(NamedTuple):
+    """Results of ``fused_linear_logprobs``; leading dimensions are x's."""
+
+    logprob: Optional[torch.Tensor]        # fp32 [...]: log p(token), 0 where ignored
+    entropy: torch.Tensor                  # fp32 [...]
+    lse: torch.Tensor                      # fp32 [...]
+    top_ids: Optional[torch.Tensor]        # int32 [..., top_k], best first
+    top_logprobs: Optional[torch.Tensor]   # fp32 [..., top_k]
+
+
+def _forward(x, weight, bias, token, h, top_k):
+    N = x.shape[0]
+    dev = x.device
+    with on_device_of(x):
+        logprob = None if token is None else torch.empty(N, dtype=torch.float32, device=dev)
+        entropy = torch.empty(N, dtype=torch.float32, device=dev)
+        lse = torch.empty(N, dtype=torch.float32, device=dev)
+        ids = top = None
+        if top_k:
+            ids = torch.empty(N, top_k, dtype=torch.int32, device=dev)
+            top = torch.empty(N, top_k, dtype=torch.float32, device=dev)
+        nbytes = B.fldce_logprob_workspace_size(h, N, top_k)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        w4 = isinstance(weight, W4Weight)
+        call = B.make_logprob_call(
+            H=x, W=None if w4 else weight, w4=weight.packed if w4 else None,
+            w4_scales=weight.scales if w4 else None, w4_group=weight.group_size if w4 else 0,
+            bias=bias, token=token, N=N, top_k=top_k, logprob=logprob, entropy=entropy, lse=lse,
+            top_ids=ids, top_logprobs=top, workspace=ws, workspace_bytes=nbytes,
+            stream=torch.cuda.current_stream(dev))
+        B.fldce_logprob(h, call)
+    return logprob, entropy, lse, ids, top
+
+
+class FusedLinearLogProbsFunction(torch.autograd.Function):
+    """log p and entropy with gradients; lse and the alternatives without."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, token, h, top_k):
+        logprob, entropy, lse, ids, top = _forward(x, weight, bias, token, h, top_k)
+        ctx.set_materialize_grads(False)
+        ctx.h = h
+        ctx.save_for_backward(x, weight, bias, token, lse, entropy)
+        ctx.mark_non_differentiable(*(t for t in (lse, ids, top) if t is not None))
+        return logprob, entropy, lse, ids, top
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dlogprob, dentropy, *_):
+        x, weight, bias, token, lse, entropy = ctx.saved_tensors
+        need_x, need_w, need_b = ctx.needs_input_grad[:3]
+        if dlogprob is None and dentropy is None:
+            return None, None, None, None, None, None
+        if dlogprob is not None:
+            dlogprob = dlogprob.float().contiguous()
+        if dentropy is not None:
+            dentropy = dentropy.float().contiguous()
+        N = x.shape[0]
+        dev = x.device
+        with on_device_of(x):
+            dH = torch.empty_like(x) if need_x else None
+            dW = torch.empty_like(weight) if need_w else None
+            db = torch.empty_like(bias) if need_b else None
+            nbytes = B.fldce_workspace_size(ctx.h, N)
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            call = B.make_logprob_grad_call(
+                H=x, W=weight, bias=bias, token=token, N=N, lse=lse, entropy=entropy,
+                dlogprob=dlogprob, dentropy=dentropy, dH=dH, dW=dW, db=db,
+                workspace=ws, workspace_bytes=nbytes,
+                stream=torch.cuda.current_stream(dev))
+            B.fldce_logprob_bwd(ctx.h, call)
+        return dH, dW, db, None, None, None
+
+
+def fused_linear_logprobs(x: torch.Tensor, token: Optional[torch.Tensor],
+                          weight: Union[torch.Tensor, W4Weight],
+                          bias: Optional[torch.Tensor] = None, *, top_k: int = 0,
+                          logit_scale: float = 1.0, ignore_index: int = -100,
+                          chunk_n: int = 0) -> LinearLogProbs:
+    """x [..., D], token [...] int64 (or None), weight [V, D] or ``W4Weight``,
+    bias [V] or None -> ``LinearLogProbs``.
+
+    z = logit_scale * (x W^T + bias).  A token equal to ``ignore_index``, or
+    outside [0, V), has logprob 0 and no gradient through it.  ``top_ids`` are
+    ordered by the exact logits, equal ones by lowest id; a bias of -inf takes
+    an entry out.  ``chunk_n`` (0: the library's choice) bounds the tokens
+    whose logit gradient the backward holds at a time.
+    """
+    w4 = isinstance(weight, W4Weight)
+    if w4:
+        check_w4_input(x, weight, bias)
+    elif weight.dim() != 2 or x.dim() < 1 or x.shape[-1] != weight.shape[1]:
+        raise ValueError(f"x {tuple(x.shape)} and weight {tuple(weight.shape)} do not match")
+    elif x.dtype != weight.dtype:
+        raise TypeError("x and weight must have the same dtype")
+    V, D = weight.shape
+    if bias is not None and (bias.shape != (V,) or bias.dtype != x.dtype):
+        raise ValueError(f"bias {tuple(bias.shape)} {bias.dtype} does not match weight")
+    if token is not None and token.shape != x.shape[:-1]:
+        raise ValueError(f"x={tuple(x.shape)}, token={tuple(token.shape)}")
+    if token is not None and (token.is_floating_point() or token.is_complex()
+                              or token.dtype == torch.bool):
+        raise TypeError(f"token has to hold integers, got {token.dtype}")
+    if not 0 <= top_k <= min(B.FLDCE_MAX_TOP_K, V):
+        raise ValueError(f"top_k {top_k} is not in 0..{min(B.FLDCE_MAX_TOP_K, V)}")
+    _dtype_code(x.dtype)
+    if not x.is_cuda:
+        raise RuntimeError("the fused log-probabilities run on CUDA tensors only")
+    for t in (weight, bias, token):
+        if t is not None and t.device != x.device:
+            raise ValueError("x, token, weight and bias are on different devices")
+    lead = x.shape[:-1]
+    x2 = dense(x.reshape(-1, D))
+    if not w4:
+        weight = dense(weight)
+    bias = dense(bias)
+    if token is not None:
+        token = token.reshape(-1).to(torch.int64).contiguous()
+    h = _handle(x.dtype, D, V, float(logit_scale), int(ignore_index), int(chunk_n))
+    if torch.is_grad_enabled() and not w4 and (
+            x2.requires_grad or weight.requires_grad or (bias is not None and bias.requires_grad)):
+        out = FusedLinearLogProbsFunction.apply(x2, weight, bias, token, h, top_k)
+    else:
+        out = _forward(x2, weight, bias, token, h, top_k)
+    if len(lead) != 1:
+        out = (*(None if t is None else t.view(lead) for t in out[:3]),
+               *(None if t is None else t.view(*lead, top_k) for t in out[3:]))
+    return LinearLogProbs(*out)
+
+
+class FusedLinearLogProbs(torch.nn.Module):
+    """``fused_linear_logprobs`` with its options held by a module."""
+
+    def __init__(self, top_k: int = 0, logit_scale: float = 1.0, ignore_index: int = -100,
+                 chunk_n: int = 0):
+        super().__init__()
+        if not 0 <= top_k <= B.FLDCE_MAX_TOP_K:
+            raise ValueError(f"top_k {top_k} is not in 0..{B.FLDCE_MAX_TOP_K}")
+        self.top_k = top_k
+        self.logit_scale = logit_scale
+        self.ignore_index = ignore_index
+        self.chunk_n = chunk_n
+
+    def forward(self, x: torch.Tensor, token: Optional[torch.Tensor],
+                weight: Union[torch.Tensor, W4Weight],
+                bias: Optional[torch.Tensor] = None) -> LinearLogProbs:
+        return fused_linear_logprobs(x, token, weight, bias, top_k=self.top_k,
+                                     logit_scale=self.logit_scale,
+                                     ignore_index=self.ignore_index, chunk_n=self.chunk_n)
