@@ -1,0 +1,452 @@
+// few.cuh -- the head's product for few tokens (up to 32 at a time), with a
+// 16-bit or a 4-bit weight: its logits, or their statistics without them.
+//
+// Bound by the bytes of the weight, which every CTA streams once: the
+// vocabulary is cut into one contiguous range of rows per SM (equal to
+// within 8 rows), so every SM reads the same bytes and there is no last
+// round.  A producer thread keeps a ring of TMA boxes in flight (up to 198 KB
+// per SM, several times bandwidth x latency) across tile boundaries; 16
+// consumer warps turn them into logits with m16n8k16 matrix instructions:
+// vocabulary rows are M and tokens are N, so one token costs an 8-column
+// product, where the 256-row tiles of the many-token sweep would spend 256.
+// A warp takes 32 rows (two M tiles share the token operand) and one half of
+// each stage's K; the halves meet in shared memory at the end of a tile.
+//
+// 4-bit weights go from shared memory to registers as 32-bit words of eight
+// nibbles.  (w >> 4 i) & 0x000f000f holds elements i and i + 4; or-ing them
+// into the mantissa of 128 (with the sign bit flipped) gives 136 + q in
+// bf16, and a subtraction of 136 is exact: the products are of integers.
+// The token operand is paired to match (elements i and i + 4) by byte
+// permutes.  A group's sum is scaled in fp32 when the group ends; with groups
+// of 32, 64 or 128 every 32-element block lies in one group.
+//
+// Sums are kept short: the matrix instruction truncates its fp32 accumulator
+// at every step, so a run of at most 128 products (or a group) is added to
+// the row's sum by a rounded fp32 addition.
+#pragma once
+#include "w4.cuh"
+
+namespace fldce {
+
+constexpr int kFewTokens = 32;          // tokens per pass
+constexpr int kFewConsumers = 16;       // warps
+constexpr int kFewThreads = 32 * (kFewConsumers + 1);
+constexpr int kFewRows = 256;           // rows of a tile at most
+constexpr int kFewMaxParts = 160;       // CTAs at most
+
+template <bool W4, int NT>
+struct FewCfg {
+    static constexpr int KS = W4 ? 256 : 64;                  // elements of K per stage
+    static constexpr int XBOXES = KS / 64;                    // 64-element boxes of x
+    static constexpr uint32_t W_BYTES = kFewRows * 128;       // a box row is 128 bytes
+    static constexpr uint32_t XBOX_BYTES = 8 * NT * 128;
+    static constexpr uint32_t STAGE_BYTES = W_BYTES + XBOXES * XBOX_BYTES;
+    // the logits of a tile: [token][row]; the pitch spreads a fragment's
+    // store over all banks
+    static constexpr int PITCH = kFewRows + (W4 ? 8 : 4);
+    static constexpr uint32_t LG_BYTES = 8 * NT * PITCH * 4;
+    static constexpr int STAGES =
+        (int)((232448u - 1024u - 256u - LG_BYTES) / STAGE_BYTES) < 6
+            ? (int)((232448u - 1024u - 256u - LG_BYTES) / STAGE_BYTES) : 6;
+    static constexpr uint32_t SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + LG_BYTES + 256;
+    static constexpr int TPW = (8 * NT + kFewConsumers - 1) / kFewConsumers;   // tokens per warp
+    static_assert(STAGES >= 4 && SMEM_BYTES <= 232448, "shared memory");
+};
+
+struct FewParams {
+    CUtensorMap wmap;          // [V, D] boxes of tile_rows x 128 bytes, 128B swizzle
+    CUtensorMap xmap;          // [n_tok, D] bf16 boxes of 8 NT x 64, 128B swizzle
+    int64_t V;
+    int cta_rows;              // vocabulary rows per CTA (a multiple of 8)
+    int tile_rows;             // rows per tile (a multiple of 8, at most 256)
+    int tiles;                 // tiles per CTA
+    int k_stages;              // ceil(D / KS)
+    int n_tok;
+    HeadWeight hw;             // scales of a 4-bit weight
+    const __nv_bfloat16* bias; // [V] or null
+    // statistics
+    float c;                   // |s| log2(e)
+    int neg;                   // s < 0
+    LpParts parts;             // rows row0 .. row0 + n_tok - 1
+    int row0;
+    // logits
+    void* out;                 // [n_tok][V]
+    int out_bf16;
+    int32_t* err;
+};
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* m, uint32_t bar,
+                                            int32_t x, int32_t y, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "l"(policy)
+        : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Elements (i, i + 4) of a word of nibbles, as bf16.
+__device__ __forceinline__ uint32_t nibble_pair(uint32_t w, int i) {
+    const uint32_t u = ((w >> (4 * i)) & 0x000f000fu) ^ 0x43084308u;      // 136 + q
+    const __nv_bfloat162 off = __halves2bfloat162(__ushort_as_bfloat16(0x4308),
+                                                  __ushort_as_bfloat16(0x4308));
+    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u), off);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ void consumers_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kFewConsumers) : "memory");
+}
+
+// KC >= 0: statistics and KC candidates per (CTA, token).  KC < 0: logits.
+template <bool W4, int NT, int KC>
+__global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ FewParams p) {
+    using Cfg = FewCfg<W4, NT>;
+    constexpr int S = Cfg::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    float* lg = reinterpret_cast<float*>(smem + S * Cfg::STAGE_BYTES);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * Cfg::STAGE_BYTES + Cfg::LG_BYTES);
+    const uint32_t sbase = smem_u32(smem);
+    auto full_bar = [&](int s) { return smem_u32(bars + s); };
+    auto empty_bar = [&](int s) { return smem_u32(bars + S + s); };
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int groups32 = (p.tile_rows + 31) / 32;           // 32-row groups of a tile
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 2 * groups32);
+        }
+        fence_mbar_init();
+        tma_prefetch_desc(&p.wmap);
+        tma_prefetch_desc(&p.xmap);
+    }
+    __syncthreads();
+    const int64_t r_begin = (int64_t)blockIdx.x * p.cta_rows;
+    const int64_t r_end = min(p.V, r_begin + p.cta_rows);
+    const int total = p.tiles * p.k_stages;
+
+    if (warp == kFewConsumers) {
+        // ------------------------------------------------ producer
+        if (lane == 0) {
+            const uint64_t pol_w = l2_policy_evict_first();     // read once
+            const uint64_t pol_x = l2_policy_evict_normal();
+            const uint32_t bytes = (uint32_t)p.tile_rows * 128u + Cfg::XBOXES * Cfg::XBOX_BYTES;
+            int it = 0;
+            bool ok = true;
+            for (int t = 0; ok && t < p.tiles; ++t) {
+                const int row = (int)(r_begin + (int64_t)t * p.tile_rows);
+                for (int k = 0; k < p.k_stages; ++k, ++it) {
+                    const int s = it % S;
+                    if (!mbar_wait_bounded(empty_bar(s), ((it / S) & 1u) ^ 1u, kWaitLimitNs)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t sw = sbase + s * Cfg::STAGE_BYTES;
+                    mbar_arrive_expect_tx(full_bar(s), bytes);
+                    // a box row is 128 bytes: 64 bf16, or 256 nibbles (128 one-byte columns)
+                    tma_load_2d(sw, &p.wmap, full_bar(s), k * (W4 ? 128 : 64), row, pol_w);
+#pragma unroll
+                    for (int b = 0; b < Cfg::XBOXES; ++b)
+                        tma_load_2d(sw + Cfg::W_BYTES + b * Cfg::XBOX_BYTES, &p.xmap, full_bar(s),
+                                    k * Cfg::KS + 64 * b, 0, pol_x);
+                }
+            }
+            if (!ok) {
+                atomicOr(p.err, FLDCE_DEV_ERR_TIMEOUT);
+                // loads in flight land before the CTA may exit (bounded again)
+                for (int i = it > S ? it - S : 0; i < it; ++i)
+                    mbar_wait_bounded(full_bar(i % S), (i / S) & 1u, kWaitLimitNs);
+            }
+        }
+        return;
+    }
+
+    // ---------------------------------------------------- consumers
+    const int rg = warp >> 1, half = warp & 1;              // 32-row group, K half
+    const int g = lane >> 2, t4 = lane & 3;
+    const bool active = rg < groups32;
+    bool ok = true;
+    RunningStats rs[Cfg::TPW];
+    WarpTop<(KC > 0 ? KC : 1)> wt[Cfg::TPW];
+
+    // scales of this thread's four rows (g, g + 8, g + 16, g + 24 of the
+    // group) for the blocks of one stage half, loaded one stage ahead
+    const int bpg = W4 ? p.hw.group / 32 : 1;               // 32-element blocks per scale
+    float sc[W4 ? 4 : 1][4], sc_next[W4 ? 4 : 1][4];
+    auto load_scales = [&](int it, float (&dst)[W4 ? 4 : 1][4]) {
+        if constexpr (W4) {
+            const int t = it / p.k_stages, k = it - t * p.k_stages;
+            const int blk0 = k * 8 + half * 4;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                int64_t v = r_begin + (int64_t)t * p.tile_rows + rg * 32 + 8 * i + g;
+                v = v < p.V ? v : p.V - 1;
+                const __nv_bfloat16* row = p.hw.scales + v * p.hw.groups;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    if (b != 0 && (b & (bpg - 1)) != 0) continue;
+                    const int gi = min((blk0 + b) / bpg, p.hw.groups - 1);
+                    dst[b][i] = __bfloat162float(__ldg(row + gi));
+                }
+            }
+        }
+    };
+    if (W4 && active) load_scales(0, sc_next);
+
+    for (int t = 0, it = 0; t < p.tiles; ++t) {
+        float acc[2][NT][4];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[m][n][e] = 0.f;
+        if (active) {
+            float part[2][NT][4];
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) part[m][n][e] = 0.f;
+            for (int k = 0; k < p.k_stages; ++k, ++it) {
+                const int s = it % S;
+                if constexpr (W4) {
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) sc[b][i] = sc_next[b][i];
+                    if (it + 1 < total) load_scales(it + 1, sc_next);
+                }
+                if (ok && !mbar_wait_bounded(full_bar(s), (it / S) & 1u, kWaitLimitNs)) {
+                    ok = false;
+                    if (lane == 0) atomicOr(p.err, FLDCE_DEV_ERR_TIMEOUT);
+                }
+                if (!ok) continue;
+                const uint32_t sw = sbase + s * Cfg::STAGE_BYTES;
+                const uint32_t sx = sw + Cfg::W_BYTES;
+                if constexpr (W4) {
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const int c = half * 4 + b;          // 16-byte chunk = 32 elements
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)          // rows 8 i + g of the group
+                            w[i] = ld_shared_u32(sw + (uint32_t)(rg * 32 + 8 * i + g) * 128u +
+                                                 (uint32_t)((c ^ g) << 4) + 4u * t4);
+                        uint32_t a[2][2][4];                 // [M tile][k16 step]
+#pragma unroll
+                        for (int m = 0; m < 2; ++m)
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                a[m][q][0] = nibble_pair(w[2 * m], 2 * q);
+                                a[m][q][1] = nibble_pair(w[2 * m + 1], 2 * q);
+                                a[m][q][2] = nibble_pair(w[2 * m], 2 * q + 1);
+                                a[m][q][3] = nibble_pair(w[2 * m + 1], 2 * q + 1);
+                            }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            // token of column g: 0 4 1 5 2 6 3 7, so that the
+                            // eight lanes of a load phase hit eight chunks
+                            const int tok = 8 * n + ((g & 1) << 2) + (g >> 1);
+                            const uint4 x = ld_shared_v4(
+                                sx + (uint32_t)(c >> 1) * Cfg::XBOX_BYTES + (uint32_t)tok * 128u +
+                                (uint32_t)((((c & 1) * 4 + t4) ^ (tok & 7)) << 4));
+                            const uint32_t p0 = __byte_perm(x.x, x.z, 0x5410);
+                            const uint32_t p1 = __byte_perm(x.x, x.z, 0x7632);
+                            const uint32_t p2 = __byte_perm(x.y, x.w, 0x5410);
+                            const uint32_t p3 = __byte_perm(x.y, x.w, 0x7632);
+#pragma unroll
+                            for (int m = 0; m < 2; ++m) {
+                                mma_bf16(part[m][n], a[m][0], p0, p1);
+                                mma_bf16(part[m][n], a[m][1], p2, p3);
+                            }
+                        }
+                        // the group ends: scale its integer products
+                        if (((b + 1) & (bpg - 1)) == 0) {
+                            const int sb = b & ~(bpg - 1);
+#pragma unroll
+                            for (int m = 0; m < 2; ++m) {
+                                float s0 = sc[0][2 * m], s1 = sc[0][2 * m + 1];
+#pragma unroll
+                                for (int j = 1; j < 4; ++j)
+                                    if (sb == j) {
+                                        s0 = sc[j][2 * m];
+                                        s1 = sc[j][2 * m + 1];
+                                    }
+#pragma unroll
+                                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        acc[m][n][e] = fmaf(part[m][n][e], e < 2 ? s0 : s1,
+                                                            acc[m][n][e]);
+                                        part[m][n][e] = 0.f;
+                                    }
+                            }
+                        }
+                    }
+                } else {
+                    uint32_t b[NT][4];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const int tok = 8 * n + (lane & 7);
+                        ldmatrix_x4(sx + (uint32_t)tok * 128u +
+                                        (uint32_t)(((half * 4 + (lane >> 3)) ^ (tok & 7)) << 4),
+                                    b[n]);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            const int row = rg * 32 + 16 * m + (lane & 15);
+                            uint32_t a[4];
+                            ldmatrix_x4(sw + (uint32_t)row * 128u +
+                                            (uint32_t)(((half * 4 + 2 * q + (lane >> 4)) ^
+                                                        (row & 7)) << 4),
+                                        a);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                mma_bf16(part[m][n], a, b[n][2 * q], b[n][2 * q + 1]);
+                        }
+                    if ((k & 3) == 3 || k + 1 == p.k_stages) {
+#pragma unroll
+                        for (int m = 0; m < 2; ++m)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    acc[m][n][e] += part[m][n][e];
+                                    part[m][n][e] = 0.f;
+                                }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty_bar(s));
+            }
+        }
+        // the K halves meet: lg[token][row]
+        auto cell = [&](int m, int n, int e) -> float* {
+            const int row = rg * 32 + 16 * m + g + (e >= 2 ? 8 : 0);
+            const int col = 2 * t4 + (e & 1);               // column of the product
+            const int tok = 8 * n + (W4 ? ((col & 1) << 2) + (col >> 1) : col);
+            return lg + tok * Cfg::PITCH + row;
+        };
+        if (active && half == 1) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) *cell(m, n, e) = acc[m][n][e];
+        }
+        consumers_sync();
+        if (active && half == 0) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) *cell(m, n, e) += acc[m][n][e];
+        }
+        consumers_sync();
+        const int64_t v0 = r_begin + (int64_t)t * p.tile_rows;
+        const int rows = (int)max((int64_t)0, min((int64_t)p.tile_rows, r_end - v0));
+#pragma unroll
+        for (int j = 0; j < Cfg::TPW; ++j) {
+            const int tok = warp + j * kFewConsumers;
+            if (tok >= p.n_tok || tok >= 8 * NT) continue;
+            for (int i0 = 0; i0 < rows; i0 += 32) {
+                const int i = i0 + lane;
+                const int64_t v = v0 + i;
+                float a = KC < 0 ? 0.f : kNegInf;
+                if (i < rows) {
+                    a = lg[tok * Cfg::PITCH + i];
+                    if (p.bias != nullptr) a += __bfloat162float(__ldg(p.bias + v));
+                    if constexpr (KC < 0) {
+                        const int64_t o = (int64_t)tok * p.V + v;
+                        if (p.out_bf16)
+                            static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(a);
+                        else
+                            static_cast<float*>(p.out)[o] = a;
+                    } else if (p.neg) {
+                        a = -a;
+                    }
+                }
+                if constexpr (KC >= 0) {
+                    const float ref = rs[j].rebase(fmaxf(rs[j].m, a), p.c);
+                    rs[j].add(a, ref, p.c);
+                    if constexpr (KC > 0) wt[j].offer(a, (int)v, lane);
+                }
+            }
+        }
+        consumers_sync();                                   // lg is free again
+    }
+    if constexpr (KC >= 0) {
+#pragma unroll
+        for (int j = 0; j < Cfg::TPW; ++j) {
+            const int tok = warp + j * kFewConsumers;
+            if (tok >= p.n_tok || tok >= 8 * NT) continue;
+            float mx = rs[j].m;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            rs[j].rebase(mx, p.c);
+            float l = rs[j].l, w = rs[j].w;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                l += __shfl_xor_sync(0xffffffffu, l, o);
+                w += __shfl_xor_sync(0xffffffffu, w, o);
+            }
+            const size_t part = blockIdx.x;
+            const int row = p.row0 + tok;
+            int n = 0;
+            if constexpr (KC > 0) {
+                const bool has = lane < KC && wt[j].v > kNegInf;
+                n = __popc(__ballot_sync(0xffffffffu, has));
+                if (has)
+                    p.parts.top[(part * KC + lane) * p.parts.ld + row] =
+                        make_float2(wt[j].v, __int_as_float(wt[j].id));
+            }
+            if (lane == 0)
+                p.parts.stats[part * p.parts.ld + row] = make_float4(mx, l, w, __int_as_float(n));
+        }
+    }
+}
+
+}  // namespace fldce

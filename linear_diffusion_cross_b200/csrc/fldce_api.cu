@@ -36,7 +36,7 @@
 #include "fused_gdh.cuh"
 #include "kernels.cuh"
 #include "logprob.cuh"
-#include "w4.cuh"
+#include "few.cuh"
 
 using namespace fldce;
 
@@ -118,7 +118,7 @@ EncodeTiledFn encode_fn() {
 }
 
 // 2-D tensor map over a row-major [outer, inner] matrix of `elt`-byte
-// elements (bf16 or fp32) with row stride `ld` elements; box = [box_outer,
+// elements (bytes, bf16 or fp32) with row stride `ld` elements; box = [box_outer,
 // box_inner], 128-byte swizzle, zero fill outside the extent.
 bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t ld,
               uint32_t box_inner, uint32_t box_outer, int elt = 2) {
@@ -128,8 +128,9 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, 
     const cuuint64_t strides[1] = {ld * (uint64_t)elt};
     const cuuint32_t box[2] = {box_inner, box_outer};
     const cuuint32_t estr[2] = {1, 1};
-    const CUtensorMapDataType dt =
-        elt == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUtensorMapDataType dt = elt == 4   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : elt == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                              : CU_TENSOR_MAP_DATA_TYPE_UINT8;
     return fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

@@ -13,22 +13,24 @@ namespace {
 
 // Partial statistics of one forward chunk: at most this much workspace.
 constexpr size_t kLpBudget = size_t(512) << 20;
-constexpr int64_t kW4PassRows = 256;            // tokens of a forward chunk on a 4-bit weight
+constexpr int64_t kW4ChunkTokens = 256;         // tokens of a forward chunk on a 4-bit weight
 
 struct LpLayout {
-    size_t cnt, stats, top, floor, logits, total;
+    size_t cnt, stats, top, floor, total;
     int64_t C;                // tokens per chunk
     int64_t n_parts;
     int kc;
+    bool few;                 // k_few instead of the tensor-core sweep's 256-row tiles
 };
 
 LpLayout lp_layout(const fldce_plan* p, int64_t N, int top_k, bool w4) {
     LpLayout L{};
     L.kc = candidates_for(top_k);
-    L.n_parts = w4 ? cdiv(p->cfg.V, kLogitPart) : p->n_vt;
+    L.few = w4 || (p->cfg.dtype == FLDCE_BF16 && N <= kFewTokens);
+    L.n_parts = L.few ? kFewMaxParts : p->n_vt;
     const size_t per_row = (size_t)L.n_parts * (16 + 8 * (size_t)L.kc);
     int64_t C = std::max<int64_t>(256, (int64_t)(kLpBudget / per_row) / 256 * 256);
-    if (w4) C = kW4PassRows;
+    if (w4) C = kW4ChunkTokens;
     L.C = std::max<int64_t>(1, std::min(C, N));
     size_t off = 0;
     auto take = [&](size_t bytes) {
@@ -40,7 +42,6 @@ LpLayout lp_layout(const fldce_plan* p, int64_t N, int top_k, bool w4) {
     L.stats = take((size_t)L.n_parts * L.C * 16);
     L.top = take((size_t)L.n_parts * L.C * L.kc * 8);
     L.floor = take((size_t)L.C * 4);
-    L.logits = take(w4 ? (size_t)kW4Tokens * p->cfg.V * 4 : 0);
     L.total = off;
     return L;
 }
@@ -60,13 +61,65 @@ HeadWeight w4_weight(const void* packed, const void* scales, int group, int64_t 
                       (int)cdiv(D, group)};
 }
 
-template <class OutT>
-cudaError_t launch_w4_rows(const __nv_bfloat16* x, int n_tok, const HeadWeight& hw,
-                           const __nv_bfloat16* bias, int64_t V, int64_t D, OutT* out, int64_t ldo,
-                           int sms, cudaStream_t st) {
-    const int blocks = (int)std::min<int64_t>(cdiv(V, 8), 8 * (int64_t)sms);
-    k_w4_rows<OutT><<<blocks, 256, 0, st>>>(x, n_tok, hw, bias, V, D, out, ldo);
+// Set a kernel's shared-memory limit once per device (as launch_gemm does).
+template <class K>
+cudaError_t allow_smem(K kern, size_t bytes, std::atomic<uint64_t>& done) {
+    int devid = 0;
+    cudaError_t e = cudaGetDevice(&devid);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = devid < 64 ? (uint64_t(1) << devid) : 0;
+    if (bit == 0 || (done.load(std::memory_order_acquire) & bit) == 0) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (e != cudaSuccess) return e;
+        done.fetch_or(bit, std::memory_order_release);
+    }
+    return cudaSuccess;
+}
+
+// How the vocabulary is cut for k_few: one range of rows per CTA, in tiles.
+struct FewGrid {
+    int ctas, cta_rows, tile_rows, tiles;
+};
+
+FewGrid few_grid(int64_t V, int sms) {
+    FewGrid g;
+    const int n = std::min(std::max(sms, 1), kFewMaxParts);
+    g.cta_rows = (int)round_up((size_t)cdiv(V, n), 8);
+    g.ctas = (int)cdiv(V, g.cta_rows);
+    g.tiles = (int)cdiv(g.cta_rows, kFewRows);
+    g.tile_rows = (int)round_up((size_t)cdiv(g.cta_rows, g.tiles), 8);
+    return g;
+}
+
+template <bool W4, int NT, int KC>
+cudaError_t launch_few_nt(FewParams& p, const FewGrid& g, const HeadWeight& hw,
+                          const __nv_bfloat16* x, int64_t D, cudaStream_t st) {
+    using Cfg = FewCfg<W4, NT>;
+    p.k_stages = (int)cdiv(D, Cfg::KS);
+    const bool maps =
+        make_map(&p.xmap, x, D, p.n_tok, D, 64, 8 * NT) &&
+        (W4 ? make_map(&p.wmap, hw.W, D / 2, p.V, D / 2, 128, g.tile_rows, 1)
+            : make_map(&p.wmap, hw.W, D, p.V, D, 64, g.tile_rows));
+    if (!maps) return cudaErrorInvalidValue;
+    static std::atomic<uint64_t> done{0};
+    auto kern = k_few<W4, NT, KC>;
+    if (cudaError_t e = allow_smem(kern, Cfg::SMEM_BYTES, done)) return e;
+    kern<<<g.ctas, kFewThreads, Cfg::SMEM_BYTES, st>>>(p);
     return cudaGetLastError();
+}
+
+// One pass over the weight for up to kFewTokens tokens.
+template <bool W4, int KC>
+cudaError_t launch_few(FewParams& p, const HeadWeight& hw, const __nv_bfloat16* x, int64_t D,
+                       int sms, cudaStream_t st) {
+    const FewGrid g = few_grid(p.V, sms);
+    p.cta_rows = g.cta_rows;
+    p.tile_rows = g.tile_rows;
+    p.tiles = g.tiles;
+    p.hw = hw;
+    if (p.n_tok <= 8) return launch_few_nt<W4, 1, KC>(p, g, hw, x, D, st);
+    if (p.n_tok <= 16) return launch_few_nt<W4, 2, KC>(p, g, hw, x, D, st);
+    return launch_few_nt<W4, 4, KC>(p, g, hw, x, D, st);
 }
 
 template <int KC>
@@ -89,19 +142,24 @@ int lp_forward(fldce_plan* h, const fldce_logprob_call& call, const LpLayout& L,
     for (int64_t r0 = 0; r0 < N; r0 += L.C) {
         const int rows = (int)std::min<int64_t>(L.C, N - r0);
         const uint8_t* Hc = static_cast<const uint8_t*>(call.H) + (size_t)r0 * D * h->elt;
-        if (KC > 0) FLDCE_CUDA(cudaMemsetAsync(parts.floor, 0, (size_t)rows * 4, st));
+        if (KC > 0 && !L.few) FLDCE_CUDA(cudaMemsetAsync(parts.floor, 0, (size_t)rows * 4, st));
         prof_mark(h, PK_GAP, st);
-        if (w4) {
+        if (L.few) {
             const __nv_bfloat16* x = reinterpret_cast<const __nv_bfloat16*>(Hc);
-            float* logits = reinterpret_cast<float*>(ws + L.logits);
-            for (int t0 = 0; t0 < rows; t0 += kW4Tokens) {
-                const int nt = std::min(kW4Tokens, rows - t0);
-                FLDCE_CUDA(launch_w4_rows<float>(x + (int64_t)t0 * D, nt, hw,
-                                                 static_cast<const __nv_bfloat16*>(call.bias), V,
-                                                 D, logits, V, dev.sms, st));
-                k_logit_parts<KC><<<(unsigned)cdiv(L.n_parts * nt, 4), 128, 0, st>>>(
-                    logits, V, nt, t0, V, c, neg, parts, (int)L.n_parts);
-                FLDCE_CUDA(cudaGetLastError());
+            FewParams fp{};
+            fp.V = V;
+            fp.bias = static_cast<const __nv_bfloat16*>(call.bias);
+            fp.c = c;
+            fp.neg = neg;
+            fp.parts = parts;
+            fp.err = &cnt->dev_err;
+            for (int t0 = 0; t0 < rows; t0 += kFewTokens) {
+                fp.n_tok = std::min(kFewTokens, rows - t0);
+                fp.row0 = t0;
+                if (w4)
+                    FLDCE_CUDA((launch_few<true, KC>(fp, hw, x + (int64_t)t0 * D, D, dev.sms, st)));
+                else
+                    FLDCE_CUDA((launch_few<false, KC>(fp, hw, x + (int64_t)t0 * D, D, dev.sms, st)));
             }
         } else if (bf16) {
             CUtensorMap mH;
@@ -121,7 +179,7 @@ int lp_forward(fldce_plan* h, const fldce_logprob_call& call, const LpLayout& L,
         prof_mark(h, PK_LSE, st);
         LpMergeParams mp{};
         mp.parts = parts;
-        mp.n_parts = (int)L.n_parts;
+        mp.n_parts = L.few ? few_grid(V, dev.sms).ctas : (int)L.n_parts;
         mp.rows = rows;
         mp.D = D;
         mp.V = V;
@@ -371,16 +429,16 @@ int fldce_w4_linear(const void* x, int64_t N, const void* packed, const void* sc
     if (int s = check_device(&dev)) return s;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const HeadWeight hw = w4_weight(packed, scales, group, D);
-    const __nv_bfloat16* xb = static_cast<const __nv_bfloat16*>(x);
-    const __nv_bfloat16* b = static_cast<const __nv_bfloat16*>(bias);
-    for (int64_t t0 = 0; t0 < N; t0 += kW4Tokens) {
-        const int nt = (int)std::min<int64_t>(kW4Tokens, N - t0);
-        if (out_dtype == FLDCE_BF16)
-            FLDCE_CUDA(launch_w4_rows(xb + t0 * D, nt, hw, b, V, D,
-                                      static_cast<__nv_bfloat16*>(out) + t0 * V, V, dev.sms, st));
-        else
-            FLDCE_CUDA(launch_w4_rows(xb + t0 * D, nt, hw, b, V, D,
-                                      static_cast<float*>(out) + t0 * V, V, dev.sms, st));
+    const size_t row_bytes = (size_t)V * (out_dtype == FLDCE_BF16 ? 2 : 4);
+    FewParams fp{};
+    fp.V = V;
+    fp.bias = static_cast<const __nv_bfloat16*>(bias);
+    fp.out_bf16 = out_dtype == FLDCE_BF16 ? 1 : 0;
+    for (int64_t t0 = 0; t0 < N; t0 += kFewTokens) {
+        fp.n_tok = (int)std::min<int64_t>(kFewTokens, N - t0);
+        fp.out = static_cast<uint8_t*>(out) + t0 * row_bytes;
+        FLDCE_CUDA((launch_few<true, -1>(fp, hw, static_cast<const __nv_bfloat16*>(x) + t0 * D, D,
+                                         dev.sms, st)));
     }
     return FLDCE_OK;
 }

@@ -1,4 +1,4 @@
-// w4.cuh -- the 4-bit head weight: quantisation and products for few tokens.
+// w4.cuh -- quantisation of the 4-bit head weight.
 //
 // W[v, d] = q[v, d] * scale[v, d / group]: q is a two's complement nibble
 // (byte i of a row holds element 2i in its low half and 2i + 1 in its high
@@ -57,103 +57,6 @@ __global__ void k_w4_quantize(const T* __restrict__ W, int64_t V, int64_t D, int
             packed[(v * D + d0 + e) / 2] = (uint8_t)b;
         }
     }
-}
-
-constexpr int kW4Tokens = 8;      // tokens per pass over the weight
-
-// Logits of up to kW4Tokens tokens, one warp per vocabulary row.
-// out[n * ldo + v] = <x_n, W_v> (+ bias[v]).
-template <class OutT>
-__global__ void __launch_bounds__(256)
-k_w4_rows(const __nv_bfloat16* __restrict__ x, int n_tok, HeadWeight hw,
-          const __nv_bfloat16* __restrict__ bias, int64_t V, int64_t D, OutT* __restrict__ out,
-          int64_t ldo) {
-    const int lane = threadIdx.x & 31;
-    const int64_t stride = (int64_t)gridDim.x * (blockDim.x >> 5);
-    for (int64_t v = blockIdx.x * (int64_t)(blockDim.x >> 5) + (threadIdx.x >> 5); v < V;
-         v += stride) {
-        float acc[kW4Tokens] = {};
-        const uint32_t* q = reinterpret_cast<const uint32_t*>(hw.W) + v * (D / 8);
-        for (int64_t i = lane; i < D / 8; i += 32) {
-            const uint32_t wq = __ldg(q + i);
-            const float sc = __bfloat162float(hw.scales[v * hw.groups + (8 * i) / hw.group]);
-            float f[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) f[k] = (float)nibble(wq, k) * sc;
-#pragma unroll
-            for (int n = 0; n < kW4Tokens; ++n) {
-                if (n >= n_tok) break;
-                const uint4 a = __ldg(reinterpret_cast<const uint4*>(x + n * D) + i);
-                const uint32_t au[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 t =
-                        __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&au[k]));
-                    acc[n] = fmaf(f[2 * k], t.x, acc[n]);
-                    acc[n] = fmaf(f[2 * k + 1], t.y, acc[n]);
-                }
-            }
-        }
-#pragma unroll
-        for (int n = 0; n < kW4Tokens; ++n) {
-            if (n >= n_tok) break;
-            float s = acc[n];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if (lane == 0) {
-                if (bias != nullptr) s += __bfloat162float(bias[v]);
-                if constexpr (sizeof(OutT) == 2) out[n * ldo + v] = __float2bfloat16_rn(s);
-                else out[n * ldo + v] = s;
-            }
-        }
-    }
-}
-
-constexpr int kLogitPart = 1024;  // columns per slice of k_logit_parts
-
-// The slices' statistics from logits in memory: one warp per (token, slice).
-// `ld` of the parts is the chunk's rows; row0 is the first token's row in it.
-template <int KC>
-__global__ void __launch_bounds__(128)
-k_logit_parts(const float* __restrict__ logits, int64_t ldl, int n_tok, int row0, int64_t V,
-              float c, int neg, LpParts parts, int n_parts) {
-    const int lane = threadIdx.x & 31;
-    const int64_t u = blockIdx.x * (int64_t)(blockDim.x >> 5) + (threadIdx.x >> 5);
-    if (u >= (int64_t)n_parts * n_tok) return;
-    const int tok = (int)(u / n_parts), part = (int)(u - (int64_t)tok * n_parts);
-    const int64_t v0 = (int64_t)part * kLogitPart;
-    const float* src = logits + tok * ldl;
-    RunningStats rs;
-    WarpTop<KC == 0 ? 1 : KC> wt;
-    for (int i = 0; i < kLogitPart; i += 32) {
-        const int64_t v = v0 + i + lane;
-        if (v0 + i >= V) break;
-        float a = -CUDART_INF_F;
-        if (v < V) a = neg ? -src[v] : src[v];
-        const float ref = rs.rebase(fmaxf(rs.m, a), c);
-        rs.add(a, ref, c);
-        if constexpr (KC > 0) wt.offer(a, (int)v, lane);
-    }
-    float mx = rs.m;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    rs.rebase(mx, c);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        rs.l += __shfl_xor_sync(0xffffffffu, rs.l, o);
-        rs.w += __shfl_xor_sync(0xffffffffu, rs.w, o);
-    }
-    int n = 0;
-    if constexpr (KC > 0) {
-        const bool has = lane < KC && wt.v > -CUDART_INF_F;
-        n = __popc(__ballot_sync(0xffffffffu, has));
-        if (has)
-            parts.top[((size_t)part * KC + lane) * parts.ld + row0 + tok] =
-                make_float2(wt.v, __int_as_float(wt.id));
-    }
-    if (lane == 0)
-        parts.stats[(size_t)part * parts.ld + row0 + tok] =
-            make_float4(mx, rs.l, rs.w, __int_as_float(n));
 }
 
 }  // namespace fldce
