@@ -438,9 +438,32 @@ Layout make_layout(const fldce_plan* p, int64_t N) {
 bool aligned16(const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; }
 bool aligned_to(const void* q, uintptr_t a) { return (reinterpret_cast<uintptr_t>(q) & (a - 1)) == 0; }
 
+// Give the calling thread the device's primary context if it has none.  A
+// thread whose first CUDA call is ours (autograd's worker, when its memory
+// comes from the allocator's cache) has none, and encoding a tensor map,
+// unlike a kernel launch, does not bind one.
+bool bind_context() {
+    using GetCurrentFn = CUresult (*)(CUcontext*);
+    static std::once_flag once;
+    static GetCurrentFn fn = nullptr;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuCtxGetCurrent", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<GetCurrentFn>(p);
+    });
+    CUcontext ctx = nullptr;
+    if (fn == nullptr) return false;
+    if (fn(&ctx) == CUDA_SUCCESS && ctx != nullptr) return true;
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
+}
+
 int check_device(DeviceInfo* d) {
     if (!device_info(d)) return FLDCE_ERR_CUDA;
     if (d->major != 10) return FLDCE_ERR_DEVICE;
+    if (!bind_context()) return FLDCE_ERR_CUDA;
     return FLDCE_OK;
 }
 

@@ -2,6 +2,7 @@
 GPU against the 64-bit definitions of tests/_logprob_ref.py, whose bounds are
 the tolerances."""
 import math
+import threading
 
 import pytest
 import torch
@@ -483,6 +484,42 @@ def test_captured_graphs_and_streams(N):
             for p, q in zip(out, want):
                 assert torch.equal(p, q)
     del graphs
+    B.fldce_destroy(h)
+
+
+@pytest.mark.parametrize("N", [4, 100])
+def test_first_cuda_call_of_a_thread(N):
+    # a new thread whose memory comes from the allocator's cache makes no CUDA
+    # call before the library's: forward and backward work there all the same
+    x, y, w, b = make(N, 128, 3000, BF, bias=True)
+    a, e = torch.randn(N, device=DEV), torch.randn(N, device=DEV)
+    ref, rref = grads_of(x, y, w, b, 1.0, a, e, top_k=3)
+    h, _ = B.fldce_create(B.FLDCE_BF16, 128, 3000, N)
+    nb = B.fldce_workspace_size(h, N)
+    ws = torch.empty(max(nb, B.fldce_logprob_workspace_size(h, N, 0)), dtype=torch.uint8, device=DEV)
+    dH, lse, ent = torch.zeros_like(x), torch.zeros(N, device=DEV), torch.zeros(N, device=DEV)
+    torch.cuda.synchronize()
+    calls = [
+        lambda: B.fldce_logprob_bwd(h, B.make_logprob_grad_call(
+            H=x, W=w, bias=b, token=y, N=N, lse=rref.lse, entropy=rref.entropy, dlogprob=a,
+            dentropy=e, dH=dH, workspace=ws, workspace_bytes=nb)),
+        lambda: B.fldce_logprob(h, B.make_logprob_call(
+            H=x, W=w, bias=b, N=N, lse=lse, entropy=ent, workspace=ws, workspace_bytes=ws.numel()))]
+    for call in calls:
+        failed = []
+
+        def body():
+            try:
+                call()
+            except Exception as exc:
+                failed.append(exc)
+
+        th = threading.Thread(target=body)
+        th.start()
+        th.join()
+        assert not failed, failed
+        torch.cuda.synchronize()
+    assert torch.equal(dH, ref[0]) and torch.equal(lse, rref.lse) and torch.equal(ent, rref.entropy)
     B.fldce_destroy(h)
 
 
