@@ -5,12 +5,13 @@
 // vocabulary is cut into one contiguous range of rows per SM (equal to
 // within 8 rows), so every SM reads the same bytes and there is no last
 // round.  A producer thread keeps a ring of TMA boxes in flight (up to 198 KB
-// per SM, several times bandwidth x latency) across tile boundaries; 16
-// consumer warps turn them into logits with m16n8k16 matrix instructions:
+// per SM, several times bandwidth x latency) across tile boundaries; 8 or
+// 16 consumer warps turn them into logits with m16n8k16 matrix instructions:
 // vocabulary rows are M and tokens are N, so one token costs an 8-column
 // product, where the 256-row tiles of the many-token sweep would spend 256.
-// A warp takes 32 rows (two M tiles share the token operand) and one half of
-// each stage's K; the halves meet in shared memory at the end of a tile.
+// A warp takes 32 rows (two M tiles share the token operand) and, up to 16
+// tokens, one half of each stage's K; the halves meet in shared memory at the
+// end of a tile.
 //
 // 4-bit weights go from shared memory to registers as 32-bit words of eight
 // nibbles.  (w >> 4 i) & 0x000f000f holds elements i and i + 4; or-ing them
@@ -29,14 +30,17 @@
 namespace fldce {
 
 constexpr int kFewTokens = 32;          // tokens per pass
-constexpr int kFewConsumers = 16;       // warps
-constexpr int kFewThreads = 32 * (kFewConsumers + 1);
 constexpr int kFewRows = 256;           // rows of a tile at most
 constexpr int kFewMaxParts = 160;       // CTAs at most
 
 template <bool W4, int NT>
 struct FewCfg {
     static constexpr int KS = W4 ? 256 : 64;                  // elements of K per stage
+    // Consumer warps: eight 32-row groups, by two K halves while the token
+    // operand and the sums leave room in the registers.
+    static constexpr int HALVES = NT <= 2 ? 2 : 1;
+    static constexpr int CONSUMERS = 8 * HALVES;
+    static constexpr int THREADS = 32 * (CONSUMERS + 1);
     static constexpr int XBOXES = KS / 64;                    // 64-element boxes of x
     static constexpr uint32_t W_BYTES = kFewRows * 128;       // a box row is 128 bytes
     static constexpr uint32_t XBOX_BYTES = 8 * NT * 128;
@@ -49,7 +53,7 @@ struct FewCfg {
         (int)((232448u - 1024u - 256u - LG_BYTES) / STAGE_BYTES) < 6
             ? (int)((232448u - 1024u - 256u - LG_BYTES) / STAGE_BYTES) : 6;
     static constexpr uint32_t SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + LG_BYTES + 256;
-    static constexpr int TPW = (8 * NT + kFewConsumers - 1) / kFewConsumers;   // tokens per warp
+    static constexpr int TPW = (8 * NT + CONSUMERS - 1) / CONSUMERS;   // tokens per warp
     static_assert(STAGES >= 4 && SMEM_BYTES <= 232448, "shared memory");
 };
 
@@ -128,15 +132,19 @@ __device__ __forceinline__ uint32_t nibble_pair(uint32_t w, int i) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+template <int THREADS>
 __device__ __forceinline__ void consumers_sync() {
-    asm volatile("bar.sync 1, %0;" ::"n"(32 * kFewConsumers) : "memory");
+    asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
 }
 
 // KC >= 0: statistics and KC candidates per (CTA, token).  KC < 0: logits.
-template <bool W4, int NT, int KC>
-__global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ FewParams p) {
+// LB: log2 of a 4-bit weight's group in 32-element blocks.
+template <bool W4, int LB, int NT, int KC>
+__global__ void __launch_bounds__(FewCfg<W4, NT>::THREADS, 1)
+k_few(const __grid_constant__ FewParams p) {
     using Cfg = FewCfg<W4, NT>;
     constexpr int S = Cfg::STAGES;
+    constexpr int HALVES = Cfg::HALVES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -151,7 +159,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(full_bar(s), 1);
-            mbar_init(empty_bar(s), 2 * groups32);
+            mbar_init(empty_bar(s), HALVES * groups32);
         }
         fence_mbar_init();
         tma_prefetch_desc(&p.wmap);
@@ -160,21 +168,20 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
     __syncthreads();
     const int64_t r_begin = (int64_t)blockIdx.x * p.cta_rows;
     const int64_t r_end = min(p.V, r_begin + p.cta_rows);
-    const int total = p.tiles * p.k_stages;
 
-    if (warp == kFewConsumers) {
+    if (warp == Cfg::CONSUMERS) {
         // ------------------------------------------------ producer
         if (lane == 0) {
             const uint64_t pol_w = l2_policy_evict_first();     // read once
             const uint64_t pol_x = l2_policy_evict_normal();
             const uint32_t bytes = (uint32_t)p.tile_rows * 128u + Cfg::XBOXES * Cfg::XBOX_BYTES;
-            int it = 0;
+            int s = 0, it = 0;
+            uint32_t ph = 1;
             bool ok = true;
             for (int t = 0; ok && t < p.tiles; ++t) {
                 const int row = (int)(r_begin + (int64_t)t * p.tile_rows);
                 for (int k = 0; k < p.k_stages; ++k, ++it) {
-                    const int s = it % S;
-                    if (!mbar_wait_bounded(empty_bar(s), ((it / S) & 1u) ^ 1u, kWaitLimitNs)) {
+                    if (!mbar_wait_bounded(empty_bar(s), ph, kWaitLimitNs)) {
                         ok = false;
                         break;
                     }
@@ -186,6 +193,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
                     for (int b = 0; b < Cfg::XBOXES; ++b)
                         tma_load_2d(sw + Cfg::W_BYTES + b * Cfg::XBOX_BYTES, &p.xmap, full_bar(s),
                                     k * Cfg::KS + 64 * b, 0, pol_x);
+                    if (++s == S) { s = 0; ph ^= 1u; }
                 }
             }
             if (!ok) {
@@ -199,78 +207,97 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
     }
 
     // ---------------------------------------------------- consumers
-    const int rg = warp >> 1, half = warp & 1;              // 32-row group, K half
+    const int rg = warp / HALVES, half = warp % HALVES;     // 32-row group, K half
     const int g = lane >> 2, t4 = lane & 3;
     const bool active = rg < groups32;
     bool ok = true;
     RunningStats rs[Cfg::TPW];
     WarpTop<(KC > 0 ? KC : 1)> wt[Cfg::TPW];
 
-    // scales of this thread's four rows (g, g + 8, g + 16, g + 24 of the
-    // group) for the blocks of one stage half, loaded one stage ahead
-    const int bpg = W4 ? p.hw.group / 32 : 1;               // 32-element blocks per scale
-    float sc[W4 ? 4 : 1][4], sc_next[W4 ? 4 : 1][4];
-    auto load_scales = [&](int it, float (&dst)[W4 ? 4 : 1][4]) {
+    // 4-bit: scales of this thread's rows (8 i + g of the group) for its
+    // blocks of one stage, as bf16 bits, loaded one stage ahead
+    constexpr int NB = 8 / HALVES;                          // 32-element blocks per stage
+    constexpr int NS = W4 ? NB >> LB : 1;                   // scales per row and stage
+    uint32_t sc_next[NS][2];                                // rows (g, g + 8), (g + 16, g + 24)
+    int sc_t = 0, sc_k = 0;                                 // stage they are for
+    auto load_scales = [&]() {
         if constexpr (W4) {
-            const int t = it / p.k_stages, k = it - t * p.k_stages;
-            const int blk0 = k * 8 + half * 4;
+            const unsigned short* base = reinterpret_cast<const unsigned short*>(p.hw.scales) +
+                                         r_begin * p.hw.groups;
+            const int last = (int)(p.V - 1 - r_begin);
+            const int r0 = sc_t * p.tile_rows + rg * 32 + g;
+            const int g0 = sc_k * (8 >> LB) + half * NS;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                int64_t v = r_begin + (int64_t)t * p.tile_rows + rg * 32 + 8 * i + g;
-                v = v < p.V ? v : p.V - 1;
-                const __nv_bfloat16* row = p.hw.scales + v * p.hw.groups;
+            for (int j = 0; j < NS; ++j) {
+                const unsigned short* col = base + min(g0 + j, p.hw.groups - 1);
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    if (b != 0 && (b & (bpg - 1)) != 0) continue;
-                    const int gi = min((blk0 + b) / bpg, p.hw.groups - 1);
-                    dst[b][i] = __bfloat162float(__ldg(row + gi));
+                for (int m = 0; m < 2; ++m) {
+                    const uint32_t lo = __ldg(col + min(r0 + 16 * m, last) * p.hw.groups);
+                    const uint32_t hi = __ldg(col + min(r0 + 16 * m + 8, last) * p.hw.groups);
+                    sc_next[j][m] = lo | (hi << 16);
                 }
             }
+            if (++sc_k == p.k_stages) { sc_k = 0; ++sc_t; }
         }
     };
-    if (W4 && active) load_scales(0, sc_next);
+    if (W4 && active) load_scales();
 
-    for (int t = 0, it = 0; t < p.tiles; ++t) {
-        float acc[2][NT][4];
+    // shared-memory offsets within a stage, the 128-byte swizzle included
+    uint32_t w_off[W4 ? 4 : 1], x_off[2];
+    const uint32_t h4 = (uint32_t)half * 4u;                // first 16-byte chunk of the half
+    // token of product column g: 0 4 1 5 2 6 3 7 (4-bit), so that the eight
+    // lanes of a 16-byte load phase hit eight different chunks
+    const uint32_t tok_g = W4 ? (uint32_t)(((g & 1) << 2) + (g >> 1)) : (uint32_t)(lane & 7);
+    if constexpr (W4) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+            w_off[b] = (uint32_t)(rg * 32 + g) * 128u + (((h4 + b) ^ g) << 4) + 4u * t4;
+        x_off[0] = Cfg::W_BYTES + (uint32_t)(half * 2) * Cfg::XBOX_BYTES + tok_g * 128u +
+                   (((uint32_t)t4 ^ tok_g) << 4);
+        x_off[1] = Cfg::W_BYTES + (uint32_t)(half * 2) * Cfg::XBOX_BYTES + tok_g * 128u +
+                   (((uint32_t)(4 + t4) ^ tok_g) << 4);
+    } else {
+        const uint32_t row = (uint32_t)(rg * 32 + (lane & 15));
+        w_off[0] = row * 128u;
+        x_off[0] = Cfg::W_BYTES + tok_g * 128u;
+        x_off[1] = 0;
+    }
+
+    int s = 0;
+    uint32_t ph = 0;
+    for (int t = 0; t < p.tiles; ++t) {
+        float acc[2][NT][4], part[2][NT][4];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[m][n][e] = 0.f;
+                for (int e = 0; e < 4; ++e) acc[m][n][e] = part[m][n][e] = 0.f;
         if (active) {
-            float part[2][NT][4];
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) part[m][n][e] = 0.f;
-            for (int k = 0; k < p.k_stages; ++k, ++it) {
-                const int s = it % S;
+            for (int k = 0; k < p.k_stages; ++k) {
+                uint32_t sc[NS][2];
                 if constexpr (W4) {
 #pragma unroll
-                    for (int b = 0; b < 4; ++b)
+                    for (int j = 0; j < NS; ++j)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) sc[b][i] = sc_next[b][i];
-                    if (it + 1 < total) load_scales(it + 1, sc_next);
+                        for (int m = 0; m < 2; ++m) sc[j][m] = sc_next[j][m];
+                    if (t + 1 < p.tiles || k + 1 < p.k_stages) load_scales();
                 }
-                if (ok && !mbar_wait_bounded(full_bar(s), (it / S) & 1u, kWaitLimitNs)) {
+                if (ok && !mbar_wait_bounded(full_bar(s), ph, kWaitLimitNs)) {
                     ok = false;
                     if (lane == 0) atomicOr(p.err, FLDCE_DEV_ERR_TIMEOUT);
                 }
                 if (!ok) continue;
-                const uint32_t sw = sbase + s * Cfg::STAGE_BYTES;
-                const uint32_t sx = sw + Cfg::W_BYTES;
+                const uint32_t st = sbase + s * Cfg::STAGE_BYTES;
                 if constexpr (W4) {
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        const int c = half * 4 + b;          // 16-byte chunk = 32 elements
+                    for (int b = 0; b < NB; ++b) {
+                        // one half: blocks 4..7 sit in the other four chunks
+                        const uint32_t wa = st + (b < 4 ? w_off[b & 3] : w_off[b & 3] ^ 64u);
                         uint32_t w[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)          // rows 8 i + g of the group
-                            w[i] = ld_shared_u32(sw + (uint32_t)(rg * 32 + 8 * i + g) * 128u +
-                                                 (uint32_t)((c ^ g) << 4) + 4u * t4);
+                            w[i] = ld_shared_u32(wa + 1024u * i);
                         uint32_t a[2][2][4];                 // [M tile][k16 step]
 #pragma unroll
                         for (int m = 0; m < 2; ++m)
@@ -283,12 +310,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
                             }
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            // token of column g: 0 4 1 5 2 6 3 7, so that the
-                            // eight lanes of a load phase hit eight chunks
-                            const int tok = 8 * n + ((g & 1) << 2) + (g >> 1);
-                            const uint4 x = ld_shared_v4(
-                                sx + (uint32_t)(c >> 1) * Cfg::XBOX_BYTES + (uint32_t)tok * 128u +
-                                (uint32_t)((((c & 1) * 4 + t4) ^ (tok & 7)) << 4));
+                            const uint4 x = ld_shared_v4(st + x_off[b & 1] +
+                                                         (b >> 1) * Cfg::XBOX_BYTES + n * 1024u);
                             const uint32_t p0 = __byte_perm(x.x, x.z, 0x5410);
                             const uint32_t p1 = __byte_perm(x.x, x.z, 0x7632);
                             const uint32_t p2 = __byte_perm(x.y, x.w, 0x5410);
@@ -299,18 +322,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
                                 mma_bf16(part[m][n], a[m][1], p2, p3);
                             }
                         }
-                        // the group ends: scale its integer products
-                        if (((b + 1) & (bpg - 1)) == 0) {
-                            const int sb = b & ~(bpg - 1);
+                        if (((b + 1) & ((1 << LB) - 1)) == 0) {
+                            // the group ends: scale its integer products
 #pragma unroll
                             for (int m = 0; m < 2; ++m) {
-                                float s0 = sc[0][2 * m], s1 = sc[0][2 * m + 1];
-#pragma unroll
-                                for (int j = 1; j < 4; ++j)
-                                    if (sb == j) {
-                                        s0 = sc[j][2 * m];
-                                        s1 = sc[j][2 * m + 1];
-                                    }
+                                const uint32_t two = sc[b >> LB][m];
+                                const float s0 = __uint_as_float(two << 16);
+                                const float s1 = __uint_as_float(two & 0xffff0000u);
 #pragma unroll
                                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -323,29 +341,28 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
                         }
                     }
                 } else {
-                    uint32_t b[NT][4];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const int tok = 8 * n + (lane & 7);
-                        ldmatrix_x4(sx + (uint32_t)tok * 128u +
-                                        (uint32_t)(((half * 4 + (lane >> 3)) ^ (tok & 7)) << 4),
-                                    b[n]);
+                    for (int q2 = 0; q2 < 2 / HALVES; ++q2) {        // 32 elements of K
+                        const uint32_t c0 = h4 + 4u * q2;            // first 16-byte chunk
+                        uint32_t b[NT][4];
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            ldmatrix_x4(st + x_off[0] + n * 1024u +
+                                            (((c0 + (lane >> 3)) ^ (lane & 7)) << 4), b[n]);
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+#pragma unroll
+                            for (int m = 0; m < 2; ++m) {
+                                uint32_t a[4];
+                                ldmatrix_x4(st + w_off[0] + 2048u * m +
+                                                (((c0 + 2u * q + (lane >> 4)) ^ (lane & 7)) << 4),
+                                            a);
+#pragma unroll
+                                for (int n = 0; n < NT; ++n)
+                                    mma_bf16(part[m][n], a, b[n][2 * q], b[n][2 * q + 1]);
+                            }
                     }
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-#pragma unroll
-                        for (int m = 0; m < 2; ++m) {
-                            const int row = rg * 32 + 16 * m + (lane & 15);
-                            uint32_t a[4];
-                            ldmatrix_x4(sw + (uint32_t)row * 128u +
-                                            (uint32_t)(((half * 4 + 2 * q + (lane >> 4)) ^
-                                                        (row & 7)) << 4),
-                                        a);
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                mma_bf16(part[m][n], a, b[n][2 * q], b[n][2 * q + 1]);
-                        }
-                    if ((k & 3) == 3 || k + 1 == p.k_stages) {
+                    if ((k & (2 * HALVES - 1)) == 2 * HALVES - 1 || k + 1 == p.k_stages) {
 #pragma unroll
                         for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -359,16 +376,17 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty_bar(s));
+                if (++s == S) { s = 0; ph ^= 1u; }
             }
         }
-        // the K halves meet: lg[token][row]
+        // the tile's logits, the K halves added: lg[token][row]
         auto cell = [&](int m, int n, int e) -> float* {
             const int row = rg * 32 + 16 * m + g + (e >= 2 ? 8 : 0);
             const int col = 2 * t4 + (e & 1);               // column of the product
             const int tok = 8 * n + (W4 ? ((col & 1) << 2) + (col >> 1) : col);
             return lg + tok * Cfg::PITCH + row;
         };
-        if (active && half == 1) {
+        if (active && half == HALVES - 1) {
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -376,8 +394,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
 #pragma unroll
                     for (int e = 0; e < 4; ++e) *cell(m, n, e) = acc[m][n][e];
         }
-        consumers_sync();
-        if (active && half == 0) {
+        consumers_sync<32 * Cfg::CONSUMERS>();
+        if (HALVES == 2 && active && half == 0) {
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -385,12 +403,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
 #pragma unroll
                     for (int e = 0; e < 4; ++e) *cell(m, n, e) += acc[m][n][e];
         }
-        consumers_sync();
+        if (HALVES == 2) consumers_sync<32 * Cfg::CONSUMERS>();
         const int64_t v0 = r_begin + (int64_t)t * p.tile_rows;
         const int rows = (int)max((int64_t)0, min((int64_t)p.tile_rows, r_end - v0));
 #pragma unroll
         for (int j = 0; j < Cfg::TPW; ++j) {
-            const int tok = warp + j * kFewConsumers;
+            const int tok = warp + j * Cfg::CONSUMERS;
             if (tok >= p.n_tok || tok >= 8 * NT) continue;
             for (int i0 = 0; i0 < rows; i0 += 32) {
                 const int i = i0 + lane;
@@ -416,12 +434,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_few(const __grid_constant__ 
                 }
             }
         }
-        consumers_sync();                                   // lg is free again
+        consumers_sync<32 * Cfg::CONSUMERS>();              // lg is free again
     }
     if constexpr (KC >= 0) {
 #pragma unroll
         for (int j = 0; j < Cfg::TPW; ++j) {
-            const int tok = warp + j * kFewConsumers;
+            const int tok = warp + j * Cfg::CONSUMERS;
             if (tok >= p.n_tok || tok >= 8 * NT) continue;
             float mx = rs[j].m;
 #pragma unroll

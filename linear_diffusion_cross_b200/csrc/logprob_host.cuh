@@ -91,7 +91,7 @@ FewGrid few_grid(int64_t V, int sms) {
     return g;
 }
 
-template <bool W4, int NT, int KC>
+template <bool W4, int LB, int NT, int KC>
 cudaError_t launch_few_nt(FewParams& p, const FewGrid& g, const HeadWeight& hw,
                           const __nv_bfloat16* x, int64_t D, cudaStream_t st) {
     using Cfg = FewCfg<W4, NT>;
@@ -102,10 +102,19 @@ cudaError_t launch_few_nt(FewParams& p, const FewGrid& g, const HeadWeight& hw,
             : make_map(&p.wmap, hw.W, D, p.V, D, 64, g.tile_rows));
     if (!maps) return cudaErrorInvalidValue;
     static std::atomic<uint64_t> done{0};
-    auto kern = k_few<W4, NT, KC>;
+    auto kern = k_few<W4, LB, NT, KC>;
     if (cudaError_t e = allow_smem(kern, Cfg::SMEM_BYTES, done)) return e;
-    kern<<<g.ctas, kFewThreads, Cfg::SMEM_BYTES, st>>>(p);
+    kern<<<g.ctas, Cfg::THREADS, Cfg::SMEM_BYTES, st>>>(p);
     return cudaGetLastError();
+}
+
+template <bool W4, int LB, int KC>
+cudaError_t launch_few_lb(FewParams& p, const FewGrid& g, const HeadWeight& hw,
+                          const __nv_bfloat16* x, int64_t D, cudaStream_t st) {
+    if (p.n_tok <= 8) return launch_few_nt<W4, LB, 1, KC>(p, g, hw, x, D, st);
+    if (p.n_tok <= 16) return launch_few_nt<W4, LB, 2, KC>(p, g, hw, x, D, st);
+    if (p.n_tok <= 24) return launch_few_nt<W4, LB, 3, KC>(p, g, hw, x, D, st);
+    return launch_few_nt<W4, LB, 4, KC>(p, g, hw, x, D, st);
 }
 
 // One pass over the weight for up to kFewTokens tokens.
@@ -117,9 +126,13 @@ cudaError_t launch_few(FewParams& p, const HeadWeight& hw, const __nv_bfloat16* 
     p.tile_rows = g.tile_rows;
     p.tiles = g.tiles;
     p.hw = hw;
-    if (p.n_tok <= 8) return launch_few_nt<W4, 1, KC>(p, g, hw, x, D, st);
-    if (p.n_tok <= 16) return launch_few_nt<W4, 2, KC>(p, g, hw, x, D, st);
-    return launch_few_nt<W4, 4, KC>(p, g, hw, x, D, st);
+    if constexpr (W4) {
+        if (hw.group == 32) return launch_few_lb<true, 0, KC>(p, g, hw, x, D, st);
+        if (hw.group == 64) return launch_few_lb<true, 1, KC>(p, g, hw, x, D, st);
+        return launch_few_lb<true, 2, KC>(p, g, hw, x, D, st);
+    } else {
+        return launch_few_lb<false, 0, KC>(p, g, hw, x, D, st);
+    }
 }
 
 template <int KC>
