@@ -58,12 +58,15 @@ struct FewCfg {
 };
 
 struct FewParams {
-    CUtensorMap wmap;          // [V, D] boxes of tile_rows x 128 bytes, 128B swizzle
+    CUtensorMap wmap;          // [V, D] boxes of kFewRows x 128 bytes, 128B swizzle
+    CUtensorMap wmap_last;     // the same in boxes of last_rows
     CUtensorMap xmap;          // [n_tok, D] bf16 boxes of 8 NT x 64, 128B swizzle
     int64_t V;
-    int cta_rows;              // vocabulary rows per CTA (a multiple of 8)
-    int tile_rows;             // rows per tile (a multiple of 8, at most 256)
-    int tiles;                 // tiles per CTA
+    // Vocabulary rows per CTA (a multiple of 8), in tiles of kFewRows and a
+    // last one of last_rows: full tiles occupy every warp.
+    int cta_rows;
+    int tiles;
+    int last_rows;
     int k_stages;              // ceil(D / KS)
     int n_tok;
     HeadWeight hw;             // scales of a 4-bit weight
@@ -123,13 +126,23 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Elements (i, i + 4) of a word of nibbles, as bf16.
-__device__ __forceinline__ uint32_t nibble_pair(uint32_t w, int i) {
-    const uint32_t u = ((w >> (4 * i)) & 0x000f000fu) ^ 0x43084308u;      // 136 + q
+// (a & mask) ^ flip in one logic instruction.
+__device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t mask, uint32_t flip) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(d) : "r"(a), "r"(mask), "r"(flip));
+    return d;
+}
+
+// Pairs (i, i + 4), i = 0..3, of a word of eight nibbles, as bf16.
+__device__ __forceinline__ void nibble_pairs(uint32_t w, uint32_t (&r)[4]) {
     const __nv_bfloat162 off = __halves2bfloat162(__ushort_as_bfloat16(0x4308),
                                                   __ushort_as_bfloat16(0x4308));
-    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u), off);
-    return *reinterpret_cast<const uint32_t*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t u = and_xor(w >> (4 * i), 0x000f000fu, 0x43084308u);   // 136 + q
+        const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u), off);
+        r[i] = *reinterpret_cast<const uint32_t*>(&d);
+    }
 }
 
 template <int THREADS>
@@ -154,15 +167,15 @@ k_few(const __grid_constant__ FewParams p) {
     auto full_bar = [&](int s) { return smem_u32(bars + s); };
     auto empty_bar = [&](int s) { return smem_u32(bars + S + s); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int groups32 = (p.tile_rows + 31) / 32;           // 32-row groups of a tile
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(full_bar(s), 1);
-            mbar_init(empty_bar(s), HALVES * groups32);
+            mbar_init(empty_bar(s), Cfg::CONSUMERS);
         }
         fence_mbar_init();
         tma_prefetch_desc(&p.wmap);
+        tma_prefetch_desc(&p.wmap_last);
         tma_prefetch_desc(&p.xmap);
     }
     __syncthreads();
@@ -174,12 +187,15 @@ k_few(const __grid_constant__ FewParams p) {
         if (lane == 0) {
             const uint64_t pol_w = l2_policy_evict_first();     // read once
             const uint64_t pol_x = l2_policy_evict_normal();
-            const uint32_t bytes = (uint32_t)p.tile_rows * 128u + Cfg::XBOXES * Cfg::XBOX_BYTES;
             int s = 0, it = 0;
             uint32_t ph = 1;
             bool ok = true;
             for (int t = 0; ok && t < p.tiles; ++t) {
-                const int row = (int)(r_begin + (int64_t)t * p.tile_rows);
+                const int row = (int)(r_begin + (int64_t)t * kFewRows);
+                const bool last = t + 1 == p.tiles;
+                const CUtensorMap* wmap = last ? &p.wmap_last : &p.wmap;
+                const uint32_t bytes = (uint32_t)(last ? p.last_rows : kFewRows) * 128u +
+                                       Cfg::XBOXES * Cfg::XBOX_BYTES;
                 for (int k = 0; k < p.k_stages; ++k, ++it) {
                     if (!mbar_wait_bounded(empty_bar(s), ph, kWaitLimitNs)) {
                         ok = false;
@@ -188,7 +204,7 @@ k_few(const __grid_constant__ FewParams p) {
                     const uint32_t sw = sbase + s * Cfg::STAGE_BYTES;
                     mbar_arrive_expect_tx(full_bar(s), bytes);
                     // a box row is 128 bytes: 64 bf16, or 256 nibbles (128 one-byte columns)
-                    tma_load_2d(sw, &p.wmap, full_bar(s), k * (W4 ? 128 : 64), row, pol_w);
+                    tma_load_2d(sw, wmap, full_bar(s), k * (W4 ? 128 : 64), row, pol_w);
 #pragma unroll
                     for (int b = 0; b < Cfg::XBOXES; ++b)
                         tma_load_2d(sw + Cfg::W_BYTES + b * Cfg::XBOX_BYTES, &p.xmap, full_bar(s),
@@ -209,7 +225,6 @@ k_few(const __grid_constant__ FewParams p) {
     // ---------------------------------------------------- consumers
     const int rg = warp / HALVES, half = warp % HALVES;     // 32-row group, K half
     const int g = lane >> 2, t4 = lane & 3;
-    const bool active = rg < groups32;
     bool ok = true;
     RunningStats rs[Cfg::TPW];
     WarpTop<(KC > 0 ? KC : 1)> wt[Cfg::TPW];
@@ -218,29 +233,33 @@ k_few(const __grid_constant__ FewParams p) {
     // blocks of one stage, as bf16 bits, loaded one stage ahead
     constexpr int NB = 8 / HALVES;                          // 32-element blocks per stage
     constexpr int NS = W4 ? NB >> LB : 1;                   // scales per row and stage
-    uint32_t sc_next[NS][2];                                // rows (g, g + 8), (g + 16, g + 24)
-    int sc_t = 0, sc_k = 0;                                 // stage they are for
+    // (not touched before that stage: a use would wait for the load)
+    unsigned short sc_next[NS][4];
+    const unsigned short* sc_base = nullptr;                // this CTA's first row of scales
+    int sc_row[4] = {};                                     // rows' offsets of the tile
+    int sc_t = -1, sc_k = 0;                                // stage loaded next
+    if constexpr (W4)
+        sc_base = reinterpret_cast<const unsigned short*>(p.hw.scales) + r_begin * p.hw.groups;
     auto load_scales = [&]() {
         if constexpr (W4) {
-            const unsigned short* base = reinterpret_cast<const unsigned short*>(p.hw.scales) +
-                                         r_begin * p.hw.groups;
-            const int last = (int)(p.V - 1 - r_begin);
-            const int r0 = sc_t * p.tile_rows + rg * 32 + g;
+            if (sc_k == 0) {
+                ++sc_t;
+                const int last = (int)(p.V - 1 - r_begin);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sc_row[i] = min(sc_t * kFewRows + rg * 32 + 8 * i + g, last) * p.hw.groups;
+            }
             const int g0 = sc_k * (8 >> LB) + half * NS;
 #pragma unroll
             for (int j = 0; j < NS; ++j) {
-                const unsigned short* col = base + min(g0 + j, p.hw.groups - 1);
+                const unsigned short* col = sc_base + min(g0 + j, p.hw.groups - 1);
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const uint32_t lo = __ldg(col + min(r0 + 16 * m, last) * p.hw.groups);
-                    const uint32_t hi = __ldg(col + min(r0 + 16 * m + 8, last) * p.hw.groups);
-                    sc_next[j][m] = lo | (hi << 16);
-                }
+                for (int i = 0; i < 4; ++i) sc_next[j][i] = __ldg(col + sc_row[i]);
             }
-            if (++sc_k == p.k_stages) { sc_k = 0; ++sc_t; }
+            if (++sc_k == p.k_stages) sc_k = 0;
         }
     };
-    if (W4 && active) load_scales();
+    if (W4) load_scales();
 
     // shared-memory offsets within a stage, the 128-byte swizzle included
     uint32_t w_off[W4 ? 4 : 1], x_off[2];
@@ -266,6 +285,8 @@ k_few(const __grid_constant__ FewParams p) {
     int s = 0;
     uint32_t ph = 0;
     for (int t = 0; t < p.tiles; ++t) {
+        const int tile_rows = t + 1 == p.tiles ? p.last_rows : kFewRows;
+        const bool active = rg * 32 < tile_rows;
         float acc[2][NT][4], part[2][NT][4];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -273,14 +294,14 @@ k_few(const __grid_constant__ FewParams p) {
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[m][n][e] = part[m][n][e] = 0.f;
-        if (active) {
-            for (int k = 0; k < p.k_stages; ++k) {
-                uint32_t sc[NS][2];
+        for (int k = 0; k < p.k_stages; ++k) {
+                float sc[NS][4];
                 if constexpr (W4) {
 #pragma unroll
                     for (int j = 0; j < NS; ++j)
 #pragma unroll
-                        for (int m = 0; m < 2; ++m) sc[j][m] = sc_next[j][m];
+                        for (int i = 0; i < 4; ++i)
+                            sc[j][i] = __uint_as_float((uint32_t)sc_next[j][i] << 16);
                     if (t + 1 < p.tiles || k + 1 < p.k_stages) load_scales();
                 }
                 if (ok && !mbar_wait_bounded(full_bar(s), ph, kWaitLimitNs)) {
@@ -288,6 +309,7 @@ k_few(const __grid_constant__ FewParams p) {
                     if (lane == 0) atomicOr(p.err, FLDCE_DEV_ERR_TIMEOUT);
                 }
                 if (!ok) continue;
+            if (active) {
                 const uint32_t st = sbase + s * Cfg::STAGE_BYTES;
                 if constexpr (W4) {
 #pragma unroll
@@ -300,14 +322,18 @@ k_few(const __grid_constant__ FewParams p) {
                             w[i] = ld_shared_u32(wa + 1024u * i);
                         uint32_t a[2][2][4];                 // [M tile][k16 step]
 #pragma unroll
-                        for (int m = 0; m < 2; ++m)
+                        for (int m = 0; m < 2; ++m) {
+                            uint32_t lo[4], hi[4];           // rows g and g + 8
+                            nibble_pairs(w[2 * m], lo);
+                            nibble_pairs(w[2 * m + 1], hi);
 #pragma unroll
                             for (int q = 0; q < 2; ++q) {
-                                a[m][q][0] = nibble_pair(w[2 * m], 2 * q);
-                                a[m][q][1] = nibble_pair(w[2 * m + 1], 2 * q);
-                                a[m][q][2] = nibble_pair(w[2 * m], 2 * q + 1);
-                                a[m][q][3] = nibble_pair(w[2 * m + 1], 2 * q + 1);
+                                a[m][q][0] = lo[2 * q];
+                                a[m][q][1] = hi[2 * q];
+                                a[m][q][2] = lo[2 * q + 1];
+                                a[m][q][3] = hi[2 * q + 1];
                             }
+                        }
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             const uint4 x = ld_shared_v4(st + x_off[b & 1] +
@@ -326,9 +352,8 @@ k_few(const __grid_constant__ FewParams p) {
                             // the group ends: scale its integer products
 #pragma unroll
                             for (int m = 0; m < 2; ++m) {
-                                const uint32_t two = sc[b >> LB][m];
-                                const float s0 = __uint_as_float(two << 16);
-                                const float s1 = __uint_as_float(two & 0xffff0000u);
+                                const float s0 = sc[b >> LB][2 * m];
+                                const float s1 = sc[b >> LB][2 * m + 1];
 #pragma unroll
                                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -374,10 +399,10 @@ k_few(const __grid_constant__ FewParams p) {
                                 }
                     }
                 }
+            }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty_bar(s));
                 if (++s == S) { s = 0; ph ^= 1u; }
-            }
         }
         // the tile's logits, the K halves added: lg[token][row]
         auto cell = [&](int m, int n, int e) -> float* {
@@ -404,8 +429,8 @@ k_few(const __grid_constant__ FewParams p) {
                     for (int e = 0; e < 4; ++e) *cell(m, n, e) += acc[m][n][e];
         }
         if (HALVES == 2) consumers_sync<32 * Cfg::CONSUMERS>();
-        const int64_t v0 = r_begin + (int64_t)t * p.tile_rows;
-        const int rows = (int)max((int64_t)0, min((int64_t)p.tile_rows, r_end - v0));
+        const int64_t v0 = r_begin + (int64_t)t * kFewRows;
+        const int rows = (int)max((int64_t)0, min((int64_t)tile_rows, r_end - v0));
 #pragma unroll
         for (int j = 0; j < Cfg::TPW; ++j) {
             const int tok = warp + j * Cfg::CONSUMERS;

@@ -76,9 +76,10 @@ cudaError_t allow_smem(K kern, size_t bytes, std::atomic<uint64_t>& done) {
     return cudaSuccess;
 }
 
-// How the vocabulary is cut for k_few: one range of rows per CTA, in tiles.
+// How the vocabulary is cut for k_few: one range of rows per CTA, in full
+// tiles and a last one.
 struct FewGrid {
-    int ctas, cta_rows, tile_rows, tiles;
+    int ctas, cta_rows, tiles, last_rows;
 };
 
 FewGrid few_grid(int64_t V, int sms) {
@@ -87,7 +88,7 @@ FewGrid few_grid(int64_t V, int sms) {
     g.cta_rows = (int)round_up((size_t)cdiv(V, n), 8);
     g.ctas = (int)cdiv(V, g.cta_rows);
     g.tiles = (int)cdiv(g.cta_rows, kFewRows);
-    g.tile_rows = (int)round_up((size_t)cdiv(g.cta_rows, g.tiles), 8);
+    g.last_rows = g.cta_rows - (g.tiles - 1) * kFewRows;
     return g;
 }
 
@@ -98,8 +99,10 @@ cudaError_t launch_few_nt(FewParams& p, const FewGrid& g, const HeadWeight& hw,
     p.k_stages = (int)cdiv(D, Cfg::KS);
     const bool maps =
         make_map(&p.xmap, x, D, p.n_tok, D, 64, 8 * NT) &&
-        (W4 ? make_map(&p.wmap, hw.W, D / 2, p.V, D / 2, 128, g.tile_rows, 1)
-            : make_map(&p.wmap, hw.W, D, p.V, D, 64, g.tile_rows));
+        (W4 ? make_map(&p.wmap, hw.W, D / 2, p.V, D / 2, 128, kFewRows, 1) &&
+                  make_map(&p.wmap_last, hw.W, D / 2, p.V, D / 2, 128, g.last_rows, 1)
+            : make_map(&p.wmap, hw.W, D, p.V, D, 64, kFewRows) &&
+                  make_map(&p.wmap_last, hw.W, D, p.V, D, 64, g.last_rows));
     if (!maps) return cudaErrorInvalidValue;
     static std::atomic<uint64_t> done{0};
     auto kern = k_few<W4, LB, NT, KC>;
@@ -123,8 +126,8 @@ cudaError_t launch_few(FewParams& p, const HeadWeight& hw, const __nv_bfloat16* 
                        int sms, cudaStream_t st) {
     const FewGrid g = few_grid(p.V, sms);
     p.cta_rows = g.cta_rows;
-    p.tile_rows = g.tile_rows;
     p.tiles = g.tiles;
+    p.last_rows = g.last_rows;
     p.hw = hw;
     if constexpr (W4) {
         if (hw.group == 32) return launch_few_lb<true, 0, KC>(p, g, hw, x, D, st);
