@@ -226,6 +226,11 @@ k_few(const __grid_constant__ FewParams p) {
     const int rg = warp / HALVES, half = warp % HALVES;     // 32-row group, K half
     const int g = lane >> 2, t4 = lane & 3;
     bool ok = true;
+    // A tile's logits of a token are read by `wpt` warps (a power of two, one
+    // when there are more tokens than warps), each a slice of its 32-row runs.
+    int wpt = 1;
+    while (2 * wpt * p.n_tok <= Cfg::CONSUMERS) wpt *= 2;
+    const int tok0 = warp / wpt, slice = warp % wpt;
     RunningStats rs[Cfg::TPW];
     WarpTop<(KC > 0 ? KC : 1)> wt[Cfg::TPW];
 
@@ -252,9 +257,10 @@ k_few(const __grid_constant__ FewParams p) {
             const int g0 = sc_k * (8 >> LB) + half * NS;
 #pragma unroll
             for (int j = 0; j < NS; ++j) {
-                const unsigned short* col = sc_base + min(g0 + j, p.hw.groups - 1);
+                const int col = min(g0 + j, p.hw.groups - 1);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sc_next[j][i] = __ldg(col + sc_row[i]);
+                for (int i = 0; i < 4; ++i)
+                    sc_next[j][i] = __ldg(sc_base + (uint32_t)(sc_row[i] + col));
             }
             if (++sc_k == p.k_stages) sc_k = 0;
         }
@@ -433,9 +439,9 @@ k_few(const __grid_constant__ FewParams p) {
         const int rows = (int)max((int64_t)0, min((int64_t)tile_rows, r_end - v0));
 #pragma unroll
         for (int j = 0; j < Cfg::TPW; ++j) {
-            const int tok = warp + j * Cfg::CONSUMERS;
-            if (tok >= p.n_tok || tok >= 8 * NT) continue;
-            for (int i0 = 0; i0 < rows; i0 += 32) {
+            const int tok = tok0 + j * Cfg::CONSUMERS;
+            if (tok >= p.n_tok) continue;
+            for (int i0 = 32 * slice; i0 < rows; i0 += 32 * wpt) {
                 const int i = i0 + lane;
                 const int64_t v = v0 + i;
                 float a = KC < 0 ? 0.f : kNegInf;
@@ -462,10 +468,14 @@ k_few(const __grid_constant__ FewParams p) {
         consumers_sync<32 * Cfg::CONSUMERS>();              // lg is free again
     }
     if constexpr (KC >= 0) {
+        // a warp's lanes, then a token's warps (through lg), become one part
+        float* sm_stats = lg;                               // [warp][3]
+        float* sm_v = lg + 3 * Cfg::CONSUMERS;              // [warp][32]
+        int* sm_id = reinterpret_cast<int*>(sm_v + 32 * Cfg::CONSUMERS);
 #pragma unroll
         for (int j = 0; j < Cfg::TPW; ++j) {
-            const int tok = warp + j * Cfg::CONSUMERS;
-            if (tok >= p.n_tok || tok >= 8 * NT) continue;
+            const int tok = tok0 + j * Cfg::CONSUMERS;
+            const bool mine = tok < p.n_tok;
             float mx = rs[j].m;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -476,6 +486,47 @@ k_few(const __grid_constant__ FewParams p) {
                 l += __shfl_xor_sync(0xffffffffu, l, o);
                 w += __shfl_xor_sync(0xffffffffu, w, o);
             }
+            if (wpt > 1) {
+                if (j > 0) break;                           // a warp has one token then
+                if (lane == 0) {
+                    sm_stats[3 * warp] = mx;
+                    sm_stats[3 * warp + 1] = l;
+                    sm_stats[3 * warp + 2] = w;
+                }
+                if (KC > 0) {
+                    sm_v[32 * warp + lane] = lane < KC ? wt[j].v : kNegInf;
+                    sm_id[32 * warp + lane] = wt[j].id;
+                }
+                consumers_sync<32 * Cfg::CONSUMERS>();
+                if (!mine || slice != 0) continue;
+                float ml = kNegInf, ll = 0.f, wl = 0.f;     // lane i < wpt: the i-th warp's
+                if (lane < wpt) {
+                    ml = sm_stats[3 * (warp + lane)];
+                    ll = sm_stats[3 * (warp + lane) + 1];
+                    wl = sm_stats[3 * (warp + lane) + 2];
+                }
+                mx = ml;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                RunningStats r;
+                r.m = ml;
+                r.l = ll;
+                r.w = wl;
+                r.rebase(mx, p.c);
+                l = r.l;
+                w = r.w;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    l += __shfl_xor_sync(0xffffffffu, l, o);
+                    w += __shfl_xor_sync(0xffffffffu, w, o);
+                }
+                if constexpr (KC > 0)
+                    for (int i = 1; i < wpt; ++i)
+                        wt[j].offer(sm_v[32 * (warp + i) + lane], sm_id[32 * (warp + i) + lane],
+                                    lane);
+            }
+            if (!mine) continue;
             const size_t part = blockIdx.x;
             const int row = p.row0 + tok;
             int n = 0;

@@ -14,10 +14,11 @@
 //
 // The alternatives' order is decided in 64 bits: every slice keeps its KC best
 // columns by the fp32 accumulator, the merge keeps the KC best of all slices
-// (KC exceeds the k asked for by 3 or more), recomputes those columns' dot
-// products in fp64 and sorts by (value, lowest id).  So ids do not depend on
-// the summation order of the matrix instructions, the tile that computed
-// them, or the number of tokens in the call.
+// (KC exceeds the k asked for by 3 or more), recomputes in fp64 the dot
+// products of the first k and of those that fp32 cannot tell from the k-th,
+// and sorts by (value, lowest id).  So ids do not depend on the summation
+// order of the matrix instructions, the tile that computed them, or the
+// number of tokens in the call.
 #pragma once
 #include "kernels.cuh"
 
@@ -26,11 +27,14 @@ namespace fldce {
 constexpr float kNegInf = -__builtin_huge_valf();
 
 // Candidates kept per slice for k alternatives.
-constexpr int candidates_for(int k) { return k == 0 ? 0 : (k == 1 ? 4 : (k <= 5 ? 8 : 24)); }
+constexpr int candidates_for(int k) {
+    return k == 0 ? 0 : (k == 1 ? 4 : (k <= 5 ? 8 : (k <= 12 ? 16 : 24)));
+}
 
-// Order-preserving map of floats to unsigned integers (0 is below every float).
+// Order-preserving map of floats to unsigned integers (0 is below every
+// float; -0 counts as +0).
 __device__ __forceinline__ uint32_t float_key(float x) {
-    const uint32_t u = __float_as_uint(x);
+    const uint32_t u = __float_as_uint(x + 0.f);
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 __device__ __forceinline__ float key_float(uint32_t k) {
@@ -42,11 +46,10 @@ struct RunningStats {
     float m = kNegInf, l = 0.f, w = 0.f;
 
     // Move the reference to nm >= m; returns the finite reference to subtract.
+    // (While m is -inf, l and w are 0, or NaN, and stay so.)
     __device__ __forceinline__ float rebase(float nm, float c) {
         const float ref = nm == -CUDART_INF_F ? 0.f : nm;
-        if (m == -CUDART_INF_F) {
-            l = w = 0.f;
-        } else {
+        if (m != -CUDART_INF_F) {
             const float d = fmaxf((m - nm) * c, -1e4f);   // finite: 2^d d is 0, not 0 * inf
             const float f = ex2(d);
             w = f * fmaf(d, l, w);
@@ -139,7 +142,8 @@ __device__ __forceinline__ void store_part(const LpParts& p, int part, int row,
 // KC best, columns equal to it still can (by a lower id).
 __device__ __forceinline__ float row_floor(const LpParts& p, int row) {
     const uint32_t k = __ldcg(&p.floor[row]);
-    return k == 0 ? -CUDART_INF_F : key_float(k - 1);
+    // (below +0 comes -0, which is not below it)
+    return k == 0 ? -CUDART_INF_F : key_float(k == 0x80000000u ? k - 2 : k - 1);
 }
 
 // ======================================================================
@@ -318,56 +322,99 @@ __device__ __forceinline__ int nibble(uint32_t w, int i) {
     return ((int)(w << (28 - 4 * i))) >> 28;       // two's complement
 }
 
-// <x, W_v> by one warp.  Products of two bf16 (and of 4-bit values) are exact
-// in fp32; products of fp32 are taken in fp64; the sum is in fp64.
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        f[2 * k] = __uint_as_float(u[k] << 16);
+        f[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+    }
+}
+
+constexpr int kDots = 4;             // rows of W per group of dot products
+
+// This thread's share of <x, W_v[j]> (z) and of sum |x_i w_i| (mag), j <
+// kDots, v[j] < 0 being skipped; the block's threads share a row, and four
+// rows' loads are in flight together.  Products of two bf16 (and of 4-bit
+// values) are exact in fp32; products of fp32 are taken in fp64; the sums are
+// in fp64.
 template <class T>
-__device__ __forceinline__ double warp_dot(const T* __restrict__ x, const HeadWeight& hw,
-                                           int64_t v, int64_t D, int lane) {
-    double s = 0.0;
+__device__ __forceinline__ void dot_share(const T* __restrict__ x, const HeadWeight& hw,
+                                          const int (&v)[kDots], int64_t D, int tid, int threads,
+                                          double (&z)[kDots], float (&mag)[kDots]) {
+#pragma unroll
+    for (int j = 0; j < kDots; ++j) { z[j] = 0.0; mag[j] = 0.f; }
     if constexpr (sizeof(T) == 2) {
         const uint4* xq = reinterpret_cast<const uint4*>(x);
-        for (int64_t i = lane; i < D / 8; i += 32) {
-            const uint4 a = __ldg(xq + i);
-            const uint32_t au[4] = {a.x, a.y, a.z, a.w};
-            float f[8];
+        const int n = (int)(D / 8);
+        if (hw.group > 0) {
+            for (int i = tid; i < n; i += threads) {
+                float f[8];
+                unpack8(__ldg(xq + i), f);
+                const int gi = (8 * i) / hw.group;
+                uint32_t w[kDots] = {};
+                float c[kDots] = {};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 t = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&au[k]));
-                f[2 * k] = t.x;
-                f[2 * k + 1] = t.y;
+                for (int j = 0; j < kDots; ++j)
+                    if (v[j] >= 0) {
+                        w[j] = __ldg(static_cast<const uint32_t*>(hw.W) + (int64_t)v[j] * n + i);
+                        c[j] = __bfloat162float(hw.scales[(int64_t)v[j] * hw.groups + gi]);
+                    }
+#pragma unroll
+                for (int j = 0; j < kDots; ++j) {
+                    if (v[j] < 0) continue;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float t = f[k] * ((float)nibble(w[j], k) * c[j]);
+                        z[j] += (double)t;
+                        mag[j] += fabsf(t);
+                    }
+                }
             }
-            if (hw.group > 0) {
-                const uint32_t q =
-                    __ldg(reinterpret_cast<const uint32_t*>(hw.W) + (v * D) / 8 + i);
-                const float sc = __bfloat162float(hw.scales[v * hw.groups + (8 * i) / hw.group]);
+        } else {
+            for (int i = tid; i < n; i += threads) {
+                float f[8];
+                unpack8(__ldg(xq + i), f);
+                uint4 w[kDots] = {};
 #pragma unroll
-                for (int k = 0; k < 8; ++k) s += (double)(f[k] * ((float)nibble(q, k) * sc));
-            } else {
-                const uint4 b = __ldg(reinterpret_cast<const uint4*>(
-                                          static_cast<const __nv_bfloat16*>(hw.W) + v * D) + i);
-                const uint32_t bu[4] = {b.x, b.y, b.z, b.w};
+                for (int j = 0; j < kDots; ++j)
+                    if (v[j] >= 0)
+                        w[j] = __ldg(reinterpret_cast<const uint4*>(hw.W) + (int64_t)v[j] * n + i);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 t =
-                        __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&bu[k]));
-                    s += (double)(f[2 * k] * t.x);
-                    s += (double)(f[2 * k + 1] * t.y);
+                for (int j = 0; j < kDots; ++j) {
+                    if (v[j] < 0) continue;
+                    float g[8];
+                    unpack8(w[j], g);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float t = f[k] * g[k];
+                        z[j] += (double)t;
+                        mag[j] += fabsf(t);
+                    }
                 }
             }
         }
     } else {
-        const float* w = static_cast<const float*>(hw.W) + v * D;
-        for (int64_t i = lane; i < D; i += 32) s += (double)x[i] * (double)__ldg(w + i);
+        for (int64_t i = tid; i < D; i += threads) {
+            const double xi = (double)x[i];
+#pragma unroll
+            for (int j = 0; j < kDots; ++j) {
+                if (v[j] < 0) continue;
+                const double t =
+                    xi * (double)__ldg(static_cast<const float*>(hw.W) + (int64_t)v[j] * D + i);
+                z[j] += t;
+                mag[j] += fabsf((float)t);
+            }
+        }
     }
-    return warp_sum(s);
 }
 
 struct LpMergeParams {
     LpParts parts;
     int n_parts;
-    int rows;
     int64_t D, V, ignore_index;
     float s, c;
+    float dot_err;                   // bound of a logit's fp32 error over sum |x_i w_i|
     const void* H;                   // chunk's hidden states [rows, D]
     HeadWeight hw;
     const void* bias;                // [V] (type of H) or null
@@ -381,71 +428,171 @@ struct LpMergeParams {
     int32_t* n_err;                  // counts tokens outside [0, V), or null
 };
 
-constexpr int kLpMergeThreads = 128;
+constexpr int kMergeKeep = 6;        // slices a thread keeps in registers
 
-// One block per row: the slices' statistics are combined in fp64, its warps
-// gather the KC best candidates, and every candidate (and the given token)
-// gets its dot product in fp64.
-template <int KC, class T>
-__global__ void __launch_bounds__(kLpMergeThreads) k_logprob_merge(const LpMergeParams p) {
-    constexpr int NW = kLpMergeThreads / 32;
+// (value, id) as one integer that is larger for what ranks first: the larger
+// value, then the lower id (0 to 2^31 - 1).  0 stands for nothing.
+__device__ __forceinline__ uint64_t rank_key(float v, int id) {
+    return (uint64_t)float_key(v) << 32 | (uint32_t)(0x7fffffff - id);
+}
+__device__ __forceinline__ float rank_value(uint64_t k) { return key_float((uint32_t)(k >> 32)); }
+__device__ __forceinline__ int rank_id(uint64_t k) { return 0x7fffffff - (int)(uint32_t)k; }
+
+__device__ __forceinline__ uint64_t warp_max(uint64_t k) {
+    const uint32_t hi = (uint32_t)(k >> 32);
+    const uint32_t m = __reduce_max_sync(0xffffffffu, hi);
+    const uint32_t lo = __reduce_max_sync(0xffffffffu, hi == m ? (uint32_t)k : 0u);
+    return (uint64_t)m << 32 | lo;
+}
+
+// The KC largest of a warp's keys, n per lane; lane r gets the r-th (0: there
+// are fewer).  Keys are distinct, and used up.
+template <int KC, int n>
+__device__ __forceinline__ uint64_t warp_draw(uint64_t (&key)[n], int lane) {
+    uint64_t out = 0;
+    for (int r = 0; r < KC; ++r) {
+        uint64_t best = key[0];
+#pragma unroll
+        for (int j = 1; j < n; ++j) best = key[j] > best ? key[j] : best;
+        best = warp_max(best);
+        if (best == 0) break;
+#pragma unroll
+        for (int j = 0; j < n; ++j) key[j] = key[j] == best ? 0 : key[j];
+        out = lane == r ? best : out;
+    }
+    return out;
+}
+
+// One block per row.
+//
+// Statistics: two passes over the slices' (m, l, w), the second in fp64.
+//
+// Candidates: a slice's m is its best column's value, so the KC best columns
+// lie in the KC slices that rank first by m (ties: by slice, which is by
+// column), and of the r-th of them only the first KC - r entries matter.
+// Warps draw the slices, then the columns, by warp-wide maxima.
+//
+// Dot products in fp64: the given token, the first k candidates, and of the
+// others those that the fp32 values cannot tell from the k-th (their distance
+// is below twice the bound of the fp32 error).  The result is sorted by the
+// fp64 values.
+//
+// Four warps share a group of dot products.  With few rows a block has four
+// such sets (THREADS = 512): the latency of one row is the kernel's, and one
+// token's 8 alternatives take 5,300 cycles of dot products instead of 12,400.
+// With many rows one set (128) leaves room for more rows per SM.
+template <int KC, class T, int THREADS>
+__global__ void __launch_bounds__(THREADS) k_logprob_merge(const LpMergeParams p) {
+    constexpr int NW = 4;                              // warps that read and draw the slices
+    constexpr int SETS = THREADS / 128;
+    constexpr int KA = KC == 0 ? 1 : KC;
+    constexpr int CHUNK = kMergeKeep * 32 * NW;
     const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     __shared__ float sm_max[NW];
     __shared__ double sm_l[NW], sm_w[NW];
-    __shared__ float sm_v[NW][32];
-    __shared__ int sm_id[NW][32];
-    __shared__ double sm_z[33];
-    __shared__ int sm_cand[33];
+    __shared__ uint64_t head_key[NW * 32];
+    __shared__ int sel_part[KA], sel_n[KA];
+    __shared__ uint64_t ent_key[KA * KA];
+    __shared__ float cand_v[KA];
+    __shared__ int cand_id[KA];
+    __shared__ double cand_z[KA + 1];                  // the given token's last
+    __shared__ float cand_abs[KA + 1];
+    __shared__ double sm_z[4][KA + 1];
+    __shared__ float sm_mag[4][KA + 1];
+    const float4* stats = p.parts.stats + row;
+    const size_t ld = p.parts.ld;
 
-    float mx = -CUDART_INF_F;
-    for (int k = tid; k < p.n_parts; k += kLpMergeThreads)
-        mx = fmaxf(mx, p.parts.stats[(size_t)k * p.parts.ld + row].x);
+    // ---- statistics: a thread's first slices stay in registers between passes
+    float4 kept[kMergeKeep];
+    float mx = kNegInf;
+    auto load_chunk = [&](int c0) {
+#pragma unroll
+        for (int j = 0; j < kMergeKeep; ++j) {
+            const int k = c0 + tid + j * 32 * NW;
+            kept[j] = warp < NW && k < p.n_parts ? stats[k * ld] : make_float4(kNegInf, 0.f, 0.f, 0.f);
+        }
+    };
+    load_chunk(0);
+#pragma unroll
+    for (int j = 0; j < kMergeKeep; ++j) mx = fmaxf(mx, kept[j].x);
+    if (warp < NW)
+        for (int k = tid + CHUNK; k < p.n_parts; k += 32 * NW) mx = fmaxf(mx, stats[k * ld].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if (lane == 0) sm_max[warp] = mx;
+    if (warp < NW && lane == 0) sm_max[warp] = mx;
+    if (tid < KC) {
+        sel_n[tid] = 0;
+        cand_id[tid] = -1;
+        cand_v[tid] = kNegInf;
+    }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < NW; ++i) mx = fmaxf(mx, sm_max[i]);
-
     double l = 0.0, w = 0.0;
-    WarpTop<KC == 0 ? 1 : KC> wt;
-    for (int k0 = 32 * warp; k0 < p.n_parts; k0 += kLpMergeThreads) {
-        const int k = k0 + lane;
-        float4 s = make_float4(-CUDART_INF_F, 0.f, 0.f, 0.f);
-        if (k < p.n_parts) s = p.parts.stats[(size_t)k * p.parts.ld + row];
-        if (s.x != -CUDART_INF_F || s.y != 0.f) {      // a slice with a logit (or a NaN)
-            const float d = fmaxf((s.x - mx) * p.c, -1e4f);
-            const double f = (double)exp2f(d);
-            l += f * s.y;
-            w += f * ((double)s.z + (double)d * s.y);
-        }
-        if constexpr (KC > 0) {
-            const int n = __float_as_int(s.w);
-            for (int e = 0; e < KC; ++e) {
-                float x = -CUDART_INF_F;
-                int id = 0x7fffffff;
-                if (e < n) {
-                    const float2 t = p.parts.top[((size_t)k * KC + e) * p.parts.ld + row];
-                    x = t.x;
-                    id = __float_as_int(t.y);
-                }
-                // lists are sorted: once no slice's e-th entry enters, none further does
-                const float kv = __shfl_sync(0xffffffffu, wt.v, KC - 1);
-                if (!__any_sync(0xffffffffu, x > -CUDART_INF_F && x >= kv)) break;
-                wt.offer(x, id, lane);
+    // Slices below the row's floor hold none of the KC best.
+    const float floor = KC > 0 && p.parts.floor != nullptr ? row_floor(p.parts, row) : kNegInf;
+    uint64_t drawn = 0;                                // lane r: the warp's r-th slice so far
+    for (int c0 = 0; warp < NW && c0 < p.n_parts; c0 += CHUNK) {
+        if (c0 > 0) load_chunk(c0);
+        uint64_t key[kMergeKeep + 1];
+#pragma unroll
+        for (int j = 0; j < kMergeKeep; ++j) {
+            const float4 s = kept[j];
+            if (s.x != kNegInf || s.y != 0.f) {        // a slice with a logit (or a NaN)
+                const float d = fmaxf((s.x - mx) * p.c, -1e4f);
+                const double f = (double)exp2f(d);
+                l += f * s.y;
+                w += f * ((double)s.z + (double)d * s.y);
             }
+            key[j] = s.x > floor && __float_as_int(s.w) > 0
+                         ? rank_key(s.x, c0 + tid + j * 32 * NW) : 0;
         }
+        key[kMergeKeep] = drawn;
+        if constexpr (KC > 0) drawn = warp_draw<KC, kMergeKeep + 1>(key, lane);
     }
     l = warp_sum(l);
     w = warp_sum(w);
-    if (lane == 0) { sm_l[warp] = l; sm_w[warp] = w; }
-    if constexpr (KC > 0) { sm_v[warp][lane] = wt.v; sm_id[warp][lane] = wt.id; }
+    if (warp < NW) {
+        if (lane == 0) { sm_l[warp] = l; sm_w[warp] = w; }
+        head_key[tid] = drawn;
+    }
     __syncthreads();
+
+    // ---- candidates
     if constexpr (KC > 0) {
         if (warp == 0) {
-            for (int i = 1; i < NW; ++i)
-                wt.offer(lane < KC ? sm_v[i][lane] : -CUDART_INF_F, sm_id[i][lane], lane);
-            sm_cand[lane] = lane < KC && wt.v > -CUDART_INF_F ? wt.id : -1;
+            uint64_t key[NW];
+#pragma unroll
+            for (int j = 0; j < NW; ++j) key[j] = head_key[lane + 32 * j];
+            const uint64_t k = warp_draw<KC, NW>(key, lane);
+            if (lane < KC && k != 0) {
+                sel_part[lane] = rank_id(k);
+                sel_n[lane] = min(KC - lane, __float_as_int(stats[rank_id(k) * ld].w));
+            }
+        }
+        __syncthreads();
+        for (int i = tid; i < KC * KC; i += THREADS) {
+            const int r = i / KC, e = i - r * KC;
+            if (e >= sel_n[r]) continue;
+            const float2 t = p.parts.top[((size_t)sel_part[r] * KC + e) * ld + row];
+            ent_key[i] = rank_key(t.x, __float_as_int(t.y));
+        }
+        __syncthreads();
+        if (warp == 0) {
+            // lane r walks the r-th slice's list
+            const int n = lane < KC ? sel_n[lane] : 0;
+            int e = 0;
+            uint64_t key = n > 0 ? ent_key[lane * KC] : 0;
+            for (int r = 0; r < KC; ++r) {
+                const uint64_t best = warp_max(key);
+                if (best == 0) break;
+                if (key == best) {
+                    cand_v[r] = rank_value(best);
+                    cand_id[r] = rank_id(best);
+                    ++e;
+                    key = e < n ? ent_key[lane * KC + e] : 0;
+                }
+            }
         }
     }
     int64_t y = -1;
@@ -456,47 +603,115 @@ __global__ void __launch_bounds__(kLpMergeThreads) k_logprob_merge(const LpMerge
             else if (tid == 0 && p.n_err != nullptr) atomicAdd(p.n_err, 1);
         }
     }
-    if (tid == 0) sm_cand[32] = (int)y;
     __syncthreads();
+
+    // ---- dot products
     const T* x = static_cast<const T*>(p.H) + (int64_t)row * p.D;
-    for (int i = warp; i <= KC; i += NW) {             // KC candidates, then the given token
-        const int slot = i == KC ? 32 : i;
-        const int v = sm_cand[slot];
-        if (v < 0) continue;                           // the same for the whole warp
-        double z = warp_dot<T>(x, p.hw, v, p.D, lane);
+    const int set = warp >> 2;
+    // kDots slots by the four warps of a set; slot KC is the given token
+    auto dots = [&](const int (&slot)[kDots], const int (&v)[kDots]) {
+        bool any = false;
+#pragma unroll
+        for (int j = 0; j < kDots; ++j) any = any || v[j] >= 0;
+        if (!any) return;                              // the same for the whole set
+        double z[kDots];
+        float mag[kDots];
+        dot_share<T>(x, p.hw, v, p.D, tid & 127, 128, z, mag);
+#pragma unroll
+        for (int j = 0; j < kDots; ++j) {
+            if (v[j] < 0) continue;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                z[j] += __shfl_xor_sync(0xffffffffu, z[j], o);
+                mag[j] += __shfl_xor_sync(0xffffffffu, mag[j], o);
+            }
+            if (lane == 0) {
+                sm_z[warp & 3][slot[j]] = z[j];
+                sm_mag[warp & 3][slot[j]] = mag[j];
+            }
+        }
+    };
+    // after a barrier: the logit of a slot that dots() was given
+    auto finish = [&](int slot, int v) {
+        float b = 0.f;
         if (p.bias != nullptr) {
             if constexpr (sizeof(T) == 2)
-                z += (double)__bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[v]);
+                b = __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[v]);
             else
-                z += (double)static_cast<const float*>(p.bias)[v];
+                b = static_cast<const float*>(p.bias)[v];
         }
-        if (lane == 0) sm_z[slot] = (double)p.s * z;
+        const double z = (sm_z[0][slot] + sm_z[1][slot]) + (sm_z[2][slot] + sm_z[3][slot]);
+        cand_z[slot] = (double)p.s * (z + (double)b);
+        cand_abs[slot] = (sm_mag[0][slot] + sm_mag[1][slot]) +
+                         (sm_mag[2][slot] + sm_mag[3][slot]) + fabsf(b);
+    };
+    const int first = KC == 0 ? 0 : p.k;               // slots 0 .. k - 1, then the token's
+    for (int i = set * kDots; i <= first; i += SETS * kDots) {
+        int slot[kDots], v[kDots];
+#pragma unroll
+        for (int j = 0; j < kDots; ++j) {
+            slot[j] = i + j == first ? KC : i + j;
+            v[j] = i + j > first ? -1 : (i + j == first ? (int)y : cand_id[i + j]);
+        }
+        dots(slot, v);
     }
     __syncthreads();
+    if (tid <= first) {
+        const int v = tid == first ? (int)y : cand_id[tid];
+        if (v >= 0) finish(tid == first ? KC : tid, v);
+    }
+    __syncthreads();
+    if constexpr (KC > 0) {
+        // a candidate past the k-th is as good as the k-th if their fp32
+        // values differ by less than both may be off
+        float mag = 0.f;
+        for (int i = 0; i < p.k; ++i)
+            if (cand_id[i] >= 0) mag = fmaxf(mag, cand_abs[i]);
+        const float least = cand_v[p.k - 1] - 2.f * p.dot_err * mag;
+        if (cand_v[p.k] >= least && cand_id[p.k] >= 0) {          // seldom
+            for (int i = p.k + set * kDots; i < KC; i += SETS * kDots) {
+                int slot[kDots], v[kDots];
+#pragma unroll
+                for (int j = 0; j < kDots; ++j) {
+                    slot[j] = i + j;
+                    v[j] = i + j < KC && cand_v[i + j] >= least ? cand_id[i + j] : -1;
+                }
+                dots(slot, v);
+            }
+            __syncthreads();
+        }
+        if (tid >= p.k && tid < KC) {
+            if (cand_id[tid] >= 0 && cand_v[tid] >= least) finish(tid, cand_id[tid]);
+            else cand_z[tid] = -CUDART_INF;
+        }
+        __syncthreads();
+    }
     if (warp != 0) return;
+
+    // ---- results
     l = sm_l[0];
     w = sm_w[0];
 #pragma unroll
     for (int i = 1; i < NW; ++i) { l += sm_l[i]; w += sm_w[i]; }
     // every logit -inf: lse = -inf, no information in the row
-    const bool none = mx == -CUDART_INF_F && l == 0.0;
+    const bool none = mx == kNegInf && l == 0.0;
     const double lnl = none ? 0.0 : log(l);
-    // |s| mx, the largest logit, in fp64
     const double lse = none ? -CUDART_INF : (double)fabsf(p.s) * (double)mx + lnl;
     if (lane == 0) {
         if (p.lse != nullptr) p.lse[row] = (float)lse;
         if (p.entropy != nullptr)
             p.entropy[row] = none ? 0.f : (float)(lnl - 0.69314718055994530942 * (w / l));
         if (p.logprob != nullptr)
-            p.logprob[row] = y < 0 ? 0.f : (none ? -CUDART_INF_F : (float)(sm_z[32] - lse));
+            p.logprob[row] = y < 0 ? 0.f : (none ? kNegInf : (float)(cand_z[KC] - lse));
     }
     if constexpr (KC > 0) {
-        const int id = sm_cand[lane];
-        const double z = id >= 0 ? sm_z[lane] : -CUDART_INF;
+        const int id = lane < KC ? cand_id[lane] : -1;
+        const double z = id >= 0 ? cand_z[lane] : -CUDART_INF;
         int rank = 0;
+#pragma unroll
         for (int j = 0; j < KC; ++j) {
-            const double zj = __shfl_sync(0xffffffffu, z, j);
-            const int ij = __shfl_sync(0xffffffffu, id, j);
+            const int ij = cand_id[j];
+            const double zj = cand_z[j];
             if (ij >= 0 && (zj > z || (zj == z && ij < id))) ++rank;
         }
         const int found = __popc(__ballot_sync(0xffffffffu, id >= 0));
@@ -506,7 +721,7 @@ __global__ void __launch_bounds__(kLpMergeThreads) k_logprob_merge(const LpMerge
         }
         if (lane >= found && lane < p.k) {             // fewer logits above -inf than asked for
             p.top_ids[(size_t)row * p.k + lane] = -1;
-            p.top_logprobs[(size_t)row * p.k + lane] = -CUDART_INF_F;
+            p.top_logprobs[(size_t)row * p.k + lane] = kNegInf;
         }
     }
 }

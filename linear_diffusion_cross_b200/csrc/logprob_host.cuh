@@ -148,7 +148,7 @@ int lp_forward(fldce_plan* h, const fldce_logprob_call& call, const LpLayout& L,
     uint8_t* ws = static_cast<uint8_t*>(call.workspace);
     Counters* cnt = reinterpret_cast<Counters*>(ws + L.cnt);
     LpParts parts{reinterpret_cast<float4*>(ws + L.stats), reinterpret_cast<float2*>(ws + L.top),
-                  reinterpret_cast<uint32_t*>(ws + L.floor), (int)L.C};
+                  L.few ? nullptr : reinterpret_cast<uint32_t*>(ws + L.floor), (int)L.C};
     const float c = fabsf(cfg.logit_scale) * 1.4426950408889634f;
     const int neg = cfg.logit_scale < 0.f ? 1 : 0;
     HeadWeight hw{call.W, nullptr, 0, 0};
@@ -196,12 +196,14 @@ int lp_forward(fldce_plan* h, const fldce_logprob_call& call, const LpLayout& L,
         LpMergeParams mp{};
         mp.parts = parts;
         mp.n_parts = L.few ? few_grid(V, dev.sms).ctas : (int)L.n_parts;
-        mp.rows = rows;
         mp.D = D;
         mp.V = V;
         mp.ignore_index = cfg.ignore_index;
         mp.s = cfg.logit_scale;
         mp.c = c;
+        // fp32 accumulation: one ulp per step, in steps of 16 products on the
+        // tensor cores (which align and cut the 16: a few ulp more), 1 otherwise
+        mp.dot_err = (bf16 ? (float)cdiv(D, 16) + 16.f : (float)D) * 1.2e-7f;
         mp.H = Hc;
         mp.hw = hw;
         mp.bias = call.bias;
@@ -213,10 +215,13 @@ int lp_forward(fldce_plan* h, const fldce_logprob_call& call, const LpLayout& L,
         mp.top_ids = KC > 0 ? call.top_ids + r0 * call.top_k : nullptr;
         mp.top_logprobs = KC > 0 ? call.top_logprobs + r0 * call.top_k : nullptr;
         mp.n_err = call.err_count;
-        if (bf16)
-            k_logprob_merge<KC, __nv_bfloat16><<<rows, kLpMergeThreads, 0, st>>>(mp);
+        // a few rows: the latency of one is the kernel's
+        if (!bf16)
+            k_logprob_merge<KC, float, 128><<<rows, 128, 0, st>>>(mp);
+        else if (rows <= kFewTokens)
+            k_logprob_merge<KC, __nv_bfloat16, 512><<<rows, 512, 0, st>>>(mp);
         else
-            k_logprob_merge<KC, float><<<rows, kLpMergeThreads, 0, st>>>(mp);
+            k_logprob_merge<KC, __nv_bfloat16, 128><<<rows, 128, 0, st>>>(mp);
         FLDCE_CUDA(cudaGetLastError());
         prof_mark(h, PK_MERGE, st);
     }
@@ -284,6 +289,7 @@ int fldce_logprob(fldce_handle h, const fldce_logprob_call* cp) {
         case 0: return lp_forward<0>(h, c, L, dev);
         case candidates_for(1): return lp_forward<candidates_for(1)>(h, c, L, dev);
         case candidates_for(5): return lp_forward<candidates_for(5)>(h, c, L, dev);
+        case candidates_for(12): return lp_forward<candidates_for(12)>(h, c, L, dev);
         default: return lp_forward<candidates_for(FLDCE_MAX_TOP_K)>(h, c, L, dev);
     }
 }

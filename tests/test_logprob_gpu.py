@@ -145,13 +145,14 @@ def test_lowest_value_bias(N):
     assert (r.entropy - math.log(600)).abs().max() <= t
 
 
-def test_nan_rows_stay_their_own():
-    x, y, w, b = make(40, 64, 600, BF, bias=True, ignored=0.0)
+@pytest.mark.parametrize("N", [12, 20, 40])
+def test_nan_rows_stay_their_own(N):
+    x, y, w, b = make(N, 64, 600, BF, bias=True, ignored=0.0)
     ok = fused_linear_logprobs(x, y, w, b, top_k=3)
     x[7, 3] = math.nan
     x[9] = math.inf
     r = fused_linear_logprobs(x, y, w, b, top_k=3)
-    keep = torch.ones(40, dtype=torch.bool, device=DEV)
+    keep = torch.ones(N, dtype=torch.bool, device=DEV)
     keep[[7, 9]] = False
     for a, c in zip(r, ok):
         assert torch.equal(a[keep], c[keep])
