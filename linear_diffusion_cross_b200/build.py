@@ -19,7 +19,7 @@ ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc", "fldce_api.cu")
 DEPS = [os.path.join(PKG, "csrc", f) for f in
         ("ptx.cuh", "umma_gemm.cuh", "fused_gdh.cuh", "kernels.cuh", "logprob.cuh", "w4.cuh",
-         "few.cuh", "logprob_host.cuh")] + [
+         "few.cuh", "sweep.cuh", "logprob_host.cuh")] + [
     os.path.join(ROOT, "include", "fldce.h")]
 LIB = os.path.join(PKG, "libfldce.so")
 

@@ -37,6 +37,7 @@
 #include "kernels.cuh"
 #include "logprob.cuh"
 #include "few.cuh"
+#include "sweep.cuh"
 
 using namespace fldce;
 

@@ -118,7 +118,11 @@ __device__ __forceinline__ float select32(const float (&a)[32], int i) {
 struct LpParts {
     float4* stats;       // [n_parts][ld]  (m, l, w, entries as int bits)
     float2* top;         // [n_parts][KC][ld]  (a, column as int bits), best first
-    uint32_t* floor;     // [ld] float_key of a value that KC columns of the row reach, or 0
+    // [KC + 1][ld] float_key or 0.  Entry i < KC: the largest m of the slices
+    // with index i modulo KC, so KC columns of the row reach the smallest of
+    // them (and few others do, once every entry stands for many slices).
+    // Entry KC: the largest KC-th value of any slice, which serves until then.
+    uint32_t* floor;
     int ld;              // rows of the chunk buffer
 };
 
@@ -133,113 +137,28 @@ __device__ __forceinline__ void store_part(const LpParts& p, int part, int row,
             if (e < n)
                 p.top[((size_t)part * KC + e) * p.ld + row] =
                     make_float2(tt.v[e], __int_as_float(tt.id[e]));
-        if (n == KC) atomicMax(&p.floor[row], float_key(tt.v[KC - 1]));
+        atomicMax(&p.floor[(size_t)(part % KC) * p.ld + row], float_key(st.m));
+        if (n == KC) atomicMax(&p.floor[(size_t)KC * p.ld + row], float_key(tt.v[KC - 1]));
     }
     p.stats[(size_t)part * p.ld + row] = make_float4(st.m, st.l, st.w, __int_as_float(n));
 }
 
-// A value just below the row's floor: columns below it cannot be among the
-// KC best, columns equal to it still can (by a lower id).
+// A value just below the key's: columns below a row's floor cannot be among
+// the KC best, columns equal to it still can (by a lower id).  Below +0 comes
+// -0, which is not below it; below -inf (and for no key) nothing does.
+__device__ __forceinline__ float below_key(uint32_t k) {
+    if (k <= 0x007fffffu) return kNegInf;              // float_key(-inf)
+    return key_float(k == 0x80000000u ? k - 2 : k - 1);
+}
+template <int KC>
 __device__ __forceinline__ float row_floor(const LpParts& p, int row) {
-    const uint32_t k = __ldcg(&p.floor[row]);
-    // (below +0 comes -0, which is not below it)
-    return k == 0 ? -CUDART_INF_F : key_float(k == 0x80000000u ? k - 2 : k - 1);
+    uint32_t k = 0xffffffffu;
+#pragma unroll
+    for (int i = 0; i < KC; ++i) k = min(k, __ldcg(&p.floor[(size_t)i * p.ld + row]));
+    return below_key(max(k, __ldcg(&p.floor[(size_t)KC * p.ld + row])));
 }
 
-// ======================================================================
-// Epilogue of the tcgen05 sweep H W^T: one thread per row summarises its 256
-// columns.  Work per column is a multiply, a max, an exponential and three
-// adds; a column enters the candidate list only if it beats the row's floor,
-// which tiles publish as they finish, so after the first tiles few do (about
-// KC ln(V / KC) of V columns).  Floors only cut candidates that cannot be in
-// the result, so the result does not depend on the order of the tiles.
-// ======================================================================
-template <int KC>
-struct LogprobEpi {
-    struct Params {
-        float c;                     // |s| log2(e)
-        int neg;                     // s < 0: a = -(x W^T + b)
-        int64_t V;
-        int rows;
-        const __nv_bfloat16* bias;   // [V] or null
-        LpParts parts;
-    };
-
-    template <class Cfg>
-    static __device__ __forceinline__ void run(const Params& p, const TileCtx& t,
-                                               const AccRow& acc, Stager&) {
-        static_assert(Cfg::NSUB == 1, "one 256-column MMA per vocabulary tile");
-        const int m = t.row0 + t.row;
-        const int64_t n0 = t.col0;
-        const bool live = m < p.rows;
-        const int ncols = (int)((p.V - n0) < Cfg::BN ? (p.V - n0) : Cfg::BN);
-        const bool edge = p.bias != nullptr || ncols < Cfg::BN;   // a may be -inf
-        const float c = p.c;
-        RunningStats rs;
-        ThreadTop<KC> tt;
-        if constexpr (KC > 0) tt.init(live ? row_floor(p.parts, m) : CUDART_INF_F);
-        for_each_chunk<Cfg::NCHUNK>(acc, [&](const uint32_t (&rin)[32], int j) {
-            float a[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) a[i] = __uint_as_float(rin[i]);
-            if (p.bias != nullptr) {
-                float b[32];
-                load_bias32(p.bias, n0 + 32 * j, p.V, b);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) a[i] += b[i];
-            }
-            if (p.neg) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) a[i] = -a[i];
-            }
-            if (32 * j + 32 > ncols) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (32 * j + i >= ncols) a[i] = -CUDART_INF_F;
-            }
-            float cm0 = fmaxf(a[0], a[1]), cm1 = fmaxf(a[2], a[3]);
-#pragma unroll
-            for (int i = 4; i < 32; i += 4) {
-                cm0 = fmax3(cm0, a[i], a[i + 1]);
-                cm1 = fmax3(cm1, a[i + 2], a[i + 3]);
-            }
-            const float cm = fmaxf(cm0, cm1);
-            const float ref = rs.rebase(fmaxf(rs.m, cm), c);
-            float l0 = 0.f, l1 = 0.f, w0 = 0.f, w1 = 0.f;
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-                float d0, d1;
-                add2(d0, d1, a[i], a[i + 1], -ref, -ref);
-                mul2(d0, d1, d0, d1, c, c);
-                if (edge) {
-                    d0 = d0 < -1e4f ? -1e4f : d0;
-                    d1 = d1 < -1e4f ? -1e4f : d1;
-                }
-                const float e0 = ex2(d0), e1 = ex2(d1);
-                add2(l0, l1, l0, l1, e0, e1);
-                fma2(w0, w1, e0, e1, d0, d1, w0, w1);
-            }
-            rs.l += l0 + l1;
-            rs.w += w0 + w1;
-            if constexpr (KC > 0) {
-                if (cm > tt.v[KC - 1]) {
-                    uint32_t mask = 0;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) mask |= (a[i] > tt.v[KC - 1] ? 1u : 0u) << i;
-                    while (mask != 0) {
-                        const int i = __ffs(mask) - 1;
-                        mask &= mask - 1;
-                        const float x = select32(a, i);
-                        if (x > tt.v[KC - 1]) tt.insert(x, (int)n0 + 32 * j + i);
-                    }
-                }
-            }
-        });
-        if (live) store_part<KC>(p.parts, (int)(n0 / Cfg::BN), m, rs, tt);
-    }
-};
-
-// The same over a 64-column tile of the fp32 CUDA-core GEMM.
+// A 64-column slice from a tile of the fp32 CUDA-core GEMM.
 template <int KC>
 struct SimtLogprob {
     float c;
@@ -254,7 +173,7 @@ struct SimtLogprob {
         const int ncols = (int)((V - n0) < kSimtTile ? (V - n0) : kSimtTile);
         RunningStats rs;
         ThreadTop<KC> tt;
-        if constexpr (KC > 0) tt.init(row_floor(parts, m0 + r));
+        if constexpr (KC > 0) tt.init(row_floor<KC>(parts, m0 + r));
         float mx = -CUDART_INF_F;
         for (int i = 0; i < ncols; ++i) {
             float a = C[r][i] + (bias != nullptr ? bias[n0 + i] : 0.f);
@@ -530,7 +449,12 @@ __global__ void __launch_bounds__(THREADS) k_logprob_merge(const LpMergeParams p
     for (int i = 0; i < NW; ++i) mx = fmaxf(mx, sm_max[i]);
     double l = 0.0, w = 0.0;
     // Slices below the row's floor hold none of the KC best.
-    const float floor = KC > 0 && p.parts.floor != nullptr ? row_floor(p.parts, row) : kNegInf;
+    float floor = kNegInf;
+    if (KC > 0 && p.parts.floor != nullptr) {
+        const uint32_t k = lane <= KC ? p.parts.floor[(size_t)lane * ld + row] : 0u;
+        const uint32_t least = __reduce_min_sync(0xffffffffu, lane < KC ? k : 0xffffffffu);
+        floor = below_key(max(least, __shfl_sync(0xffffffffu, k, KC)));
+    }
     uint64_t drawn = 0;                                // lane r: the warp's r-th slice so far
     for (int c0 = 0; warp < NW && c0 < p.n_parts; c0 += CHUNK) {
         if (c0 > 0) load_chunk(c0);

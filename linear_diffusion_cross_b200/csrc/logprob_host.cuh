@@ -12,7 +12,7 @@
 namespace {
 
 // Partial statistics of one forward chunk: at most this much workspace.
-constexpr size_t kLpBudget = size_t(512) << 20;
+constexpr size_t kLpBudget = size_t(1) << 30;
 constexpr int64_t kW4ChunkTokens = 256;         // tokens of a forward chunk on a 4-bit weight
 
 struct LpLayout {
@@ -27,7 +27,7 @@ LpLayout lp_layout(const fldce_plan* p, int64_t N, int top_k, bool w4) {
     LpLayout L{};
     L.kc = candidates_for(top_k);
     L.few = w4 || (p->cfg.dtype == FLDCE_BF16 && N <= kFewTokens);
-    L.n_parts = L.few ? kFewMaxParts : p->n_vt;
+    L.n_parts = L.few ? kFewMaxParts : cdiv(p->cfg.V, p->cfg.dtype == FLDCE_BF16 ? kSliceCols : kSimtTile);
     const size_t per_row = (size_t)L.n_parts * (16 + 8 * (size_t)L.kc);
     int64_t C = std::max<int64_t>(256, (int64_t)(kLpBudget / per_row) / 256 * 256);
     if (w4) C = kW4ChunkTokens;
@@ -41,7 +41,7 @@ LpLayout lp_layout(const fldce_plan* p, int64_t N, int top_k, bool w4) {
     L.cnt = take(sizeof(Counters));
     L.stats = take((size_t)L.n_parts * L.C * 16);
     L.top = take((size_t)L.n_parts * L.C * L.kc * 8);
-    L.floor = take((size_t)L.C * 4);
+    L.floor = take((size_t)L.C * 4 * (L.kc + 1));
     L.total = off;
     return L;
 }
@@ -139,6 +139,27 @@ cudaError_t launch_few(FewParams& p, const HeadWeight& hw, const __nv_bfloat16* 
 }
 
 template <int KC>
+cudaError_t launch_sweep(const CUtensorMap& h, const CUtensorMap& w, int rows, int64_t V, int64_t D,
+                         const SweepParams<KC>& sp, int32_t* err, int sms, cudaStream_t st) {
+    using Cfg = CfgKK;
+    GemmGeom g{};
+    g.tiles_m = (int)cdiv(rows, Cfg::PAIR_M);
+    g.tiles_n = (int)cdiv(V, Cfg::BN);
+    g.k_iters = (int)cdiv(D, Cfg::BK);
+    g.k_splits = 1;
+    g.num_tiles = g.tiles_m * g.tiles_n;
+    g.n_fastest = 0;
+    g.group = walk_group(g.tiles_m, (size_t)Cfg::PAIR_M * D * 2, kL2BudgetSweep);
+    static std::atomic<uint64_t> done{0};
+    auto kern = k_logprob_sweep<Cfg, KC>;
+    constexpr size_t smem = 1024 + Cfg::STAGES * Cfg::STAGE_BYTES + Cfg::BAR_BYTES;
+    if (cudaError_t e = allow_smem(kern, smem, done)) return e;
+    const int pairs = std::min(g.num_tiles, std::max(1, sms / 2));
+    kern<<<2 * pairs, kSweepThreads, smem, st>>>(h, w, g, sp, err);
+    return cudaGetLastError();
+}
+
+template <int KC>
 int lp_forward(fldce_plan* h, const fldce_logprob_call& call, const LpLayout& L,
                const DeviceInfo& dev) {
     const fldce_config& cfg = h->cfg;
@@ -158,7 +179,8 @@ int lp_forward(fldce_plan* h, const fldce_logprob_call& call, const LpLayout& L,
     for (int64_t r0 = 0; r0 < N; r0 += L.C) {
         const int rows = (int)std::min<int64_t>(L.C, N - r0);
         const uint8_t* Hc = static_cast<const uint8_t*>(call.H) + (size_t)r0 * D * h->elt;
-        if (KC > 0 && !L.few) FLDCE_CUDA(cudaMemsetAsync(parts.floor, 0, (size_t)rows * 4, st));
+        if (KC > 0 && !L.few)
+            FLDCE_CUDA(cudaMemsetAsync(parts.floor, 0, (size_t)L.C * 4 * (KC + 1), st));
         prof_mark(h, PK_GAP, st);
         if (L.few) {
             const __nv_bfloat16* x = reinterpret_cast<const __nv_bfloat16*>(Hc);
@@ -180,12 +202,9 @@ int lp_forward(fldce_plan* h, const fldce_logprob_call& call, const LpLayout& L,
         } else if (bf16) {
             CUtensorMap mH;
             if (!make_map(&mH, Hc, D, rows, D, 64, 128)) return FLDCE_ERR_CUDA;
-            typename LogprobEpi<KC>::Params ep{
+            const SweepParams<KC> sp{
                 c, neg, V, rows, static_cast<const __nv_bfloat16*>(call.bias), parts};
-            const Walk walk{0, 1, walk_group(cdiv(rows, CfgKK::PAIR_M),
-                                             (size_t)CfgKK::PAIR_M * D * 2, kL2BudgetSweep)};
-            FLDCE_CUDA((launch_gemm<CfgKK, LogprobEpi<KC>>(mH, mW, rows, V, D, walk, ep,
-                                                           &cnt->dev_err, dev.sms, st)));
+            FLDCE_CUDA(launch_sweep<KC>(mH, mW, rows, V, D, sp, &cnt->dev_err, dev.sms, st));
         } else {
             SimtLogprob<KC> e{c, neg, V, rows, static_cast<const float*>(call.bias), parts};
             FLDCE_CUDA(launch_simt(reinterpret_cast<const float*>(Hc), D, 1,
