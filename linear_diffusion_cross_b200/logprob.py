@@ -12,6 +12,7 @@ calls on several streams, and captured graphs, share none.
 """
 from __future__ import annotations
 
+import functools
 from typing import NamedTuple, Optional, Union
 
 import torch
@@ -19,10 +20,11 @@ from torch.autograd.function import once_differentiable
 
 from . import binding as B
 from .module import _dtype_code
-from .w4 import W4Weight, check_w4_input, dense, on_device_of
+from .w4 import W4Weight, check_w4_input, dense, on_device_of, raw_stream
 
 _MAX_N = (1 << 31) - 1
 _HANDLES = {}
+_INTS = frozenset((torch.int64, torch.int32, torch.int16, torch.int8, torch.uint8))
 
 
 def _handle(dtype: torch.dtype, D: int, V: int, logit_scale: float, ignore_index: int,
@@ -47,27 +49,40 @@ class LinearLogProbs(NamedTuple):
     top_logprobs: Optional[torch.Tensor]   # fp32 [..., top_k]
 
 
+@functools.lru_cache(maxsize=4096)
+def _workspace_size(h: int, N: int, top_k: int) -> int:
+    return B.fldce_logprob_workspace_size(h, N, top_k)
+
+
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
 def _forward(x, weight, bias, token, h, top_k):
     N = x.shape[0]
     dev = x.device
+    f32 = torch.float32
     with on_device_of(x):
-        logprob = None if token is None else torch.empty(N, dtype=torch.float32, device=dev)
-        entropy = torch.empty(N, dtype=torch.float32, device=dev)
-        lse = torch.empty(N, dtype=torch.float32, device=dev)
+        logprob = None if token is None else torch.empty(N, dtype=f32, device=dev)
+        entropy = torch.empty(N, dtype=f32, device=dev)
+        lse = torch.empty(N, dtype=f32, device=dev)
         ids = top = None
         if top_k:
-            ids = torch.empty(N, top_k, dtype=torch.int32, device=dev)
-            top = torch.empty(N, top_k, dtype=torch.float32, device=dev)
-        nbytes = B.fldce_logprob_workspace_size(h, N, top_k)
+            ids = torch.empty((N, top_k), dtype=torch.int32, device=dev)
+            top = torch.empty((N, top_k), dtype=f32, device=dev)
+        if N == 0:
+            return logprob, entropy, lse, ids, top
+        nbytes = _workspace_size(h, N, top_k)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        w4 = isinstance(weight, W4Weight)
-        call = B.make_logprob_call(
-            H=x, W=None if w4 else weight, w4=weight.packed if w4 else None,
-            w4_scales=weight.scales if w4 else None, w4_group=weight.group_size if w4 else 0,
-            bias=bias, token=token, N=N, top_k=top_k, logprob=logprob, entropy=entropy, lse=lse,
-            top_ids=ids, top_logprobs=top, workspace=ws, workspace_bytes=nbytes,
-            stream=torch.cuda.current_stream(dev))
-        B.fldce_logprob(h, call)
+        if isinstance(weight, W4Weight):
+            w, w4, scales, group = None, weight.packed.data_ptr(), weight.scales.data_ptr(), \
+                weight.group_size
+        else:
+            w, w4, scales, group = weight.data_ptr(), None, None, 0
+        B.fldce_logprob(h, B.fldce_logprob_call(
+            x.data_ptr(), w, w4, scales, _ptr(bias), _ptr(token), N, group, top_k, _ptr(logprob),
+            entropy.data_ptr(), lse.data_ptr(), _ptr(ids), _ptr(top), ws.data_ptr(), nbytes, None,
+            raw_stream(dev)))
     return logprob, entropy, lse, ids, top
 
 
@@ -137,24 +152,27 @@ def fused_linear_logprobs(x: torch.Tensor, token: Optional[torch.Tensor],
         raise ValueError(f"bias {tuple(bias.shape)} {bias.dtype} does not match weight")
     if token is not None and token.shape != x.shape[:-1]:
         raise ValueError(f"x={tuple(x.shape)}, token={tuple(token.shape)}")
-    if token is not None and (token.is_floating_point() or token.is_complex()
-                              or token.dtype == torch.bool):
+    if token is not None and token.dtype not in _INTS:
         raise TypeError(f"token has to hold integers, got {token.dtype}")
     if not 0 <= top_k <= min(B.FLDCE_MAX_TOP_K, V):
         raise ValueError(f"top_k {top_k} is not in 0..{min(B.FLDCE_MAX_TOP_K, V)}")
     _dtype_code(x.dtype)
     if not x.is_cuda:
         raise RuntimeError("the fused log-probabilities run on CUDA tensors only")
-    for t in (weight, bias, token):
-        if t is not None and t.device != x.device:
-            raise ValueError("x, token, weight and bias are on different devices")
+    dev = x.device
+    if weight.device != dev or (bias is not None and bias.device != dev) or (
+            token is not None and token.device != dev):
+        raise ValueError("x, token, weight and bias are on different devices")
     lead = x.shape[:-1]
-    x2 = dense(x.reshape(-1, D))
+    x2 = dense(x if len(lead) == 1 else x.reshape(-1, D))
     if not w4:
         weight = dense(weight)
     bias = dense(bias)
     if token is not None:
-        token = token.reshape(-1).to(torch.int64).contiguous()
+        if len(lead) != 1:
+            token = token.reshape(-1)
+        if token.dtype != torch.int64 or not token.is_contiguous():
+            token = token.to(torch.int64).contiguous()
     h = _handle(x.dtype, D, V, float(logit_scale), int(ignore_index), int(chunk_n))
     if torch.is_grad_enabled() and not w4 and (
             x2.requires_grad or weight.requires_grad or (bias is not None and bias.requires_grad)):

@@ -24,8 +24,15 @@ def dense(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
     """``t`` contiguous from a 16-byte boundary on, as the library takes it."""
     if t is None:
         return None
-    t = t.contiguous()
+    if not t.is_contiguous():
+        t = t.contiguous()
     return t.clone() if t.data_ptr() % 16 else t
+
+
+def raw_stream(device: torch.device) -> int:
+    """The handle of the device's current stream (for a call a token, without
+    the Stream object that torch.cuda.current_stream makes)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 class on_device_of:
@@ -60,20 +67,24 @@ class W4Weight:
             raise ValueError(f"group_size {g} is not one of {GROUP_SIZES}")
         if p.dim() != 2 or p.dtype != torch.uint8:
             raise TypeError(f"packed has to be a uint8 matrix, got {p.dtype} {tuple(p.shape)}")
-        V, D = p.shape[0], 2 * p.shape[1]
-        if D == 0 or D % 32:
-            raise ValueError(f"a 4-bit weight needs D a multiple of 32, got {D}")
+        V, D = p.shape
+        D *= 2
+        if V == 0 or D == 0 or D % 32:
+            raise ValueError(f"a 4-bit weight needs D a multiple of 32 and V > 0, got {(V, D)}")
         if s.dtype != torch.bfloat16 or s.shape != (V, -(-D // g)):
             raise ValueError(f"scales have to be bfloat16 {(V, -(-D // g))}, got {s.dtype} "
                              f"{tuple(s.shape)}")
         if p.device != s.device:
             raise ValueError("packed and scales are on different devices")
-        object.__setattr__(self, "packed", dense(p))
-        object.__setattr__(self, "scales", dense(s))
+        for name, t in (("packed", p), ("scales", s)):
+            d = dense(t)
+            if d is not t:
+                object.__setattr__(self, name, d)
 
     @property
-    def shape(self) -> torch.Size:
-        return torch.Size((self.packed.shape[0], 2 * self.packed.shape[1]))
+    def shape(self) -> tuple:
+        V, half = self.packed.shape
+        return V, 2 * half
 
     @property
     def device(self) -> torch.device:
@@ -126,10 +137,10 @@ def linear_w4(x: torch.Tensor, weight: W4Weight, bias: Optional[torch.Tensor] = 
     if weight.device != x.device or (bias is not None and bias.device != x.device):
         raise ValueError("x, weight and bias are on different devices")
     V, D = weight.shape
-    x2 = dense(x.reshape(-1, D))
+    x2 = dense(x if x.dim() == 2 else x.reshape(-1, D))
     bias = dense(bias)
     with on_device_of(x2):
-        out = torch.empty(x2.shape[0], V, dtype=out_dtype, device=x.device)
+        out = torch.empty((x2.shape[0], V), dtype=out_dtype, device=x.device)
         B.fldce_w4_linear(x2, x2.shape[0], weight.packed, weight.scales, weight.group_size, bias,
-                          V, D, out, code, torch.cuda.current_stream(x.device))
+                          V, D, out, code, raw_stream(x.device))
     return out if x.dim() == 2 else out.view(*x.shape[:-1], V)
