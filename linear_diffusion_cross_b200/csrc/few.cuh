@@ -33,7 +33,7 @@ constexpr int kFewTokens = 32;          // tokens per pass
 constexpr int kFewRows = 256;           // rows of a tile at most
 constexpr int kFewMaxParts = 160;       // CTAs at most
 
-template <bool W4, int NT>
+template <bool W4, int LB, int NT>
 struct FewCfg {
     static constexpr int KS = W4 ? 256 : 64;                  // elements of K per stage
     // Consumer warps: eight 32-row groups, by two K halves while the token
@@ -44,7 +44,10 @@ struct FewCfg {
     static constexpr int XBOXES = KS / 64;                    // 64-element boxes of x
     static constexpr uint32_t W_BYTES = kFewRows * 128;       // a box row is 128 bytes
     static constexpr uint32_t XBOX_BYTES = 8 * NT * 128;
-    static constexpr uint32_t STAGE_BYTES = W_BYTES + XBOXES * XBOX_BYTES;
+    static constexpr int NG = W4 ? 8 >> LB : 0;               // scales per row and stage
+    static constexpr uint32_t SCALE_BYTES = W4 ? kFewRows * NG * 2 : 0;
+    static constexpr uint32_t SCALE_OFF = W_BYTES + XBOXES * XBOX_BYTES;
+    static constexpr uint32_t STAGE_BYTES = SCALE_OFF + SCALE_BYTES;
     // the logits of a tile: [token][row]; the pitch spreads a fragment's
     // store over all banks
     static constexpr int PITCH = kFewRows + (W4 ? 8 : 4);
@@ -54,7 +57,7 @@ struct FewCfg {
             ? (int)((232448u - 1024u - 256u - LG_BYTES) / STAGE_BYTES) : 6;
     static constexpr uint32_t SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + LG_BYTES + 256;
     static constexpr int TPW = (8 * NT + CONSUMERS - 1) / CONSUMERS;   // tokens per warp
-    static_assert(STAGES >= 4 && SMEM_BYTES <= 232448, "shared memory");
+    static_assert(STAGES >= 3 && STAGE_BYTES % 1024 == 0 && SMEM_BYTES <= 232448, "shared memory");
 };
 
 struct FewParams {
@@ -145,6 +148,43 @@ __device__ __forceinline__ void nibble_pairs(uint32_t w, uint32_t (&r)[4]) {
     }
 }
 
+// Copy N bytes (4, 8 or 16) global -> shared asynchronously.
+template <int N>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N)
+                 : "memory");
+}
+// Arrive on `bar` when this thread's copies so far have landed (the barrier's
+// count includes the arrival).
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void st_shared_u16(uint32_t addr, unsigned short v) {
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
+}
+
+// N 16-bit values at addr, two to a word.
+template <int N>
+__device__ __forceinline__ void ld_shared_u16s(uint32_t addr, uint32_t (&w)[(N + 1) / 2]) {
+    if constexpr (N == 1) {
+        unsigned short h;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(addr) : "memory");
+        w[0] = h;
+    } else if constexpr (N == 2) {
+        w[0] = ld_shared_u32(addr);
+    } else if constexpr (N == 4) {
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr)
+                     : "memory");
+    } else {
+        const uint4 v = ld_shared_v4(addr);
+        w[0] = v.x;
+        w[1] = v.y;
+        w[2] = v.z;
+        w[3] = v.w;
+    }
+}
+
 template <int THREADS>
 __device__ __forceinline__ void consumers_sync() {
     asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
@@ -153,9 +193,9 @@ __device__ __forceinline__ void consumers_sync() {
 // KC >= 0: statistics and KC candidates per (CTA, token).  KC < 0: logits.
 // LB: log2 of a 4-bit weight's group in 32-element blocks.
 template <bool W4, int LB, int NT, int KC>
-__global__ void __launch_bounds__(FewCfg<W4, NT>::THREADS, 1)
+__global__ void __launch_bounds__(FewCfg<W4, LB, NT>::THREADS, 1)
 k_few(const __grid_constant__ FewParams p) {
-    using Cfg = FewCfg<W4, NT>;
+    using Cfg = FewCfg<W4, LB, NT>;
     constexpr int S = Cfg::STAGES;
     constexpr int HALVES = Cfg::HALVES;
     extern __shared__ uint8_t smem_raw[];
@@ -170,7 +210,7 @@ k_few(const __grid_constant__ FewParams p) {
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(full_bar(s), 1);
+            mbar_init(full_bar(s), W4 ? 33 : 1);             // the boxes; 32 lanes' scales
             mbar_init(empty_bar(s), Cfg::CONSUMERS);
         }
         fence_mbar_init();
@@ -184,40 +224,71 @@ k_few(const __grid_constant__ FewParams p) {
 
     if (warp == Cfg::CONSUMERS) {
         // ------------------------------------------------ producer
-        if (lane == 0) {
-            const uint64_t pol_w = l2_policy_evict_first();     // read once
-            const uint64_t pol_x = l2_policy_evict_normal();
-            int s = 0, it = 0;
-            uint32_t ph = 1;
-            bool ok = true;
-            for (int t = 0; ok && t < p.tiles; ++t) {
-                const int row = (int)(r_begin + (int64_t)t * kFewRows);
-                const bool last = t + 1 == p.tiles;
-                const CUtensorMap* wmap = last ? &p.wmap_last : &p.wmap;
-                const uint32_t bytes = (uint32_t)(last ? p.last_rows : kFewRows) * 128u +
-                                       Cfg::XBOXES * Cfg::XBOX_BYTES;
-                for (int k = 0; k < p.k_stages; ++k, ++it) {
-                    if (!mbar_wait_bounded(empty_bar(s), ph, kWaitLimitNs)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t sw = sbase + s * Cfg::STAGE_BYTES;
+        const uint64_t pol_w = l2_policy_evict_first();         // read once
+        const uint64_t pol_x = l2_policy_evict_normal();
+        // scales of a row and stage as one asynchronous copy where they are
+        // aligned for it (D a multiple of 256), else element by element
+        const bool whole = W4 && p.hw.groups % (W4 ? Cfg::NG : 1) == 0 &&
+                           (reinterpret_cast<uintptr_t>(p.hw.scales) % (2 * Cfg::NG + !W4)) == 0;
+        int s = 0, it = 0;
+        uint32_t ph = 1;
+        bool ok = true;
+        for (int t = 0; ok && t < p.tiles; ++t) {
+            const int64_t row0 = r_begin + (int64_t)t * kFewRows;
+            const bool last = t + 1 == p.tiles;
+            const CUtensorMap* wmap = last ? &p.wmap_last : &p.wmap;
+            const int tile_rows = last ? p.last_rows : kFewRows;
+            const uint32_t bytes = (uint32_t)tile_rows * 128u + Cfg::XBOXES * Cfg::XBOX_BYTES;
+            const unsigned short* src[W4 ? 8 : 1];           // scales of rows lane + 32 i
+            if constexpr (W4) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    src[i] = reinterpret_cast<const unsigned short*>(p.hw.scales) +
+                             min(row0 + lane + 32 * i, p.V - 1) * p.hw.groups;
+            }
+            for (int k = 0; k < p.k_stages; ++k, ++it) {
+                if (!mbar_wait_bounded(empty_bar(s), ph, kWaitLimitNs)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t sw = sbase + s * Cfg::STAGE_BYTES;
+                if (lane == 0) {
                     mbar_arrive_expect_tx(full_bar(s), bytes);
                     // a box row is 128 bytes: 64 bf16, or 256 nibbles (128 one-byte columns)
-                    tma_load_2d(sw, wmap, full_bar(s), k * (W4 ? 128 : 64), row, pol_w);
+                    tma_load_2d(sw, wmap, full_bar(s), k * (W4 ? 128 : 64), (int)row0, pol_w);
 #pragma unroll
                     for (int b = 0; b < Cfg::XBOXES; ++b)
                         tma_load_2d(sw + Cfg::W_BYTES + b * Cfg::XBOX_BYTES, &p.xmap, full_bar(s),
                                     k * Cfg::KS + 64 * b, 0, pol_x);
-                    if (++s == S) { s = 0; ph ^= 1u; }
                 }
+                if constexpr (W4) {
+                    __syncwarp();
+                    const uint32_t dst = sw + Cfg::SCALE_OFF + (uint32_t)lane * 2 * Cfg::NG;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (32 * i >= tile_rows) break;
+                        const uint32_t d = dst + (uint32_t)(64 * i * Cfg::NG);
+                        if (whole) {
+                            cp_async<2 * Cfg::NG>(d, src[i]);
+                            src[i] += Cfg::NG;
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < Cfg::NG; ++j)
+                                st_shared_u16(d + 2 * j, __ldg(src[i] + min(k * Cfg::NG + j,
+                                                                           p.hw.groups - 1)));
+                        }
+                    }
+                    if (whole) cp_async_arrive(full_bar(s));
+                    else mbar_arrive(full_bar(s));
+                }
+                if (++s == S) { s = 0; ph ^= 1u; }
             }
-            if (!ok) {
-                atomicOr(p.err, FLDCE_DEV_ERR_TIMEOUT);
-                // loads in flight land before the CTA may exit (bounded again)
-                for (int i = it > S ? it - S : 0; i < it; ++i)
-                    mbar_wait_bounded(full_bar(i % S), (i / S) & 1u, kWaitLimitNs);
-            }
+        }
+        if (!ok) {
+            if (lane == 0) atomicOr(p.err, FLDCE_DEV_ERR_TIMEOUT);
+            // loads in flight land before the CTA may exit (bounded again)
+            for (int i = it > S ? it - S : 0; i < it; ++i)
+                mbar_wait_bounded(full_bar(i % S), (i / S) & 1u, kWaitLimitNs);
         }
         return;
     }
@@ -234,38 +305,8 @@ k_few(const __grid_constant__ FewParams p) {
     RunningStats rs[Cfg::TPW];
     WarpTop<(KC > 0 ? KC : 1)> wt[Cfg::TPW];
 
-    // 4-bit: scales of this thread's rows (8 i + g of the group) for its
-    // blocks of one stage, as bf16 bits, loaded one stage ahead
     constexpr int NB = 8 / HALVES;                          // 32-element blocks per stage
-    constexpr int NS = W4 ? NB >> LB : 1;                   // scales per row and stage
-    // (not touched before that stage: a use would wait for the load)
-    unsigned short sc_next[NS][4];
-    const unsigned short* sc_base = nullptr;                // this CTA's first row of scales
-    int sc_row[4] = {};                                     // rows' offsets of the tile
-    int sc_t = -1, sc_k = 0;                                // stage loaded next
-    if constexpr (W4)
-        sc_base = reinterpret_cast<const unsigned short*>(p.hw.scales) + r_begin * p.hw.groups;
-    auto load_scales = [&]() {
-        if constexpr (W4) {
-            if (sc_k == 0) {
-                ++sc_t;
-                const int last = (int)(p.V - 1 - r_begin);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    sc_row[i] = min(sc_t * kFewRows + rg * 32 + 8 * i + g, last) * p.hw.groups;
-            }
-            const int g0 = sc_k * (8 >> LB) + half * NS;
-#pragma unroll
-            for (int j = 0; j < NS; ++j) {
-                const int col = min(g0 + j, p.hw.groups - 1);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    sc_next[j][i] = __ldg(sc_base + (uint32_t)(sc_row[i] + col));
-            }
-            if (++sc_k == p.k_stages) sc_k = 0;
-        }
-    };
-    if (W4) load_scales();
+    constexpr int NS = W4 ? NB >> LB : 1;                   // scales per row and stage half
 
     // shared-memory offsets within a stage, the 128-byte swizzle included
     uint32_t w_off[W4 ? 4 : 1], x_off[2];
@@ -301,15 +342,6 @@ k_few(const __grid_constant__ FewParams p) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[m][n][e] = part[m][n][e] = 0.f;
         for (int k = 0; k < p.k_stages; ++k) {
-                float sc[NS][4];
-                if constexpr (W4) {
-#pragma unroll
-                    for (int j = 0; j < NS; ++j)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            sc[j][i] = __uint_as_float((uint32_t)sc_next[j][i] << 16);
-                    if (t + 1 < p.tiles || k + 1 < p.k_stages) load_scales();
-                }
                 if (ok && !mbar_wait_bounded(full_bar(s), ph, kWaitLimitNs)) {
                     ok = false;
                     if (lane == 0) atomicOr(p.err, FLDCE_DEV_ERR_TIMEOUT);
@@ -318,6 +350,13 @@ k_few(const __grid_constant__ FewParams p) {
             if (active) {
                 const uint32_t st = sbase + s * Cfg::STAGE_BYTES;
                 if constexpr (W4) {
+                    // scales of this thread's rows (8 i + g of the group), two to a word
+                    uint32_t sc[4][(NS + 1) / 2];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        ld_shared_u16s<NS>(st + Cfg::SCALE_OFF +
+                                               (uint32_t)((rg * 32 + 8 * i + g) * Cfg::NG +
+                                                          half * NS) * 2, sc[i]);
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
                         // one half: blocks 4..7 sit in the other four chunks
@@ -358,8 +397,10 @@ k_few(const __grid_constant__ FewParams p) {
                             // the group ends: scale its integer products
 #pragma unroll
                             for (int m = 0; m < 2; ++m) {
-                                const float s0 = sc[b >> LB][2 * m];
-                                const float s1 = sc[b >> LB][2 * m + 1];
+                                const int j = b >> LB;
+                                const uint32_t w0 = sc[2 * m][j / 2], w1 = sc[2 * m + 1][j / 2];
+                                const float s0 = __uint_as_float((j & 1) ? w0 & 0xffff0000u : w0 << 16);
+                                const float s1 = __uint_as_float((j & 1) ? w1 & 0xffff0000u : w1 << 16);
 #pragma unroll
                                 for (int n = 0; n < NT; ++n)
 #pragma unroll

@@ -95,7 +95,7 @@ FewGrid few_grid(int64_t V, int sms) {
 template <bool W4, int LB, int NT, int KC>
 cudaError_t launch_few_nt(FewParams& p, const FewGrid& g, const HeadWeight& hw,
                           const __nv_bfloat16* x, int64_t D, cudaStream_t st) {
-    using Cfg = FewCfg<W4, NT>;
+    using Cfg = FewCfg<W4, LB, NT>;
     p.k_stages = (int)cdiv(D, Cfg::KS);
     const bool maps =
         make_map(&p.xmap, x, D, p.n_tok, D, 64, 8 * NT) &&
