@@ -466,6 +466,16 @@ k_few(const __grid_constant__ FewParams p) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) *cell(m, n, e) = acc[m][n][e];
         }
+        // this lane's rows of the tile, and their bias (asked for before the
+        // barrier): i = 32 (slice + wpt j) + lane
+        const int64_t v0 = r_begin + (int64_t)t * kFewRows;
+        const int rows = (int)max((int64_t)0, min((int64_t)tile_rows, r_end - v0));
+        float bias[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = 32 * (slice + wpt * j) + lane;
+            bias[j] = p.bias != nullptr && i < rows ? __bfloat162float(__ldg(p.bias + v0 + i)) : 0.f;
+        }
         consumers_sync<32 * Cfg::CONSUMERS>();
         if (HALVES == 2 && active && half == 0) {
 #pragma unroll
@@ -476,33 +486,43 @@ k_few(const __grid_constant__ FewParams p) {
                     for (int e = 0; e < 4; ++e) *cell(m, n, e) += acc[m][n][e];
         }
         if (HALVES == 2) consumers_sync<32 * Cfg::CONSUMERS>();
-        const int64_t v0 = r_begin + (int64_t)t * kFewRows;
-        const int rows = (int)max((int64_t)0, min((int64_t)tile_rows, r_end - v0));
 #pragma unroll
-        for (int j = 0; j < Cfg::TPW; ++j) {
-            const int tok = tok0 + j * Cfg::CONSUMERS;
+        for (int q = 0; q < Cfg::TPW; ++q) {
+            const int tok = tok0 + q * Cfg::CONSUMERS;
             if (tok >= p.n_tok) continue;
-            for (int i0 = 32 * slice; i0 < rows; i0 += 32 * wpt) {
-                const int i = i0 + lane;
-                const int64_t v = v0 + i;
-                float a = KC < 0 ? 0.f : kNegInf;
-                if (i < rows) {
-                    a = lg[tok * Cfg::PITCH + i];
-                    if (p.bias != nullptr) a += __bfloat162float(__ldg(p.bias + v));
-                    if constexpr (KC < 0) {
-                        const int64_t o = (int64_t)tok * p.V + v;
-                        if (p.out_bf16)
-                            static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(a);
-                        else
-                            static_cast<float*>(p.out)[o] = a;
-                    } else if (p.neg) {
-                        a = -a;
-                    }
+            const float* src = lg + tok * Cfg::PITCH;
+            float a[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int i = 32 * (slice + wpt * j) + lane;
+                a[j] = i < rows ? src[i] + bias[j] : kNegInf;
+            }
+            if constexpr (KC < 0) {
+                const int64_t o = (int64_t)tok * p.V + v0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int i = 32 * (slice + wpt * j) + lane;
+                    if (i >= rows) continue;
+                    if (p.out_bf16)
+                        static_cast<__nv_bfloat16*>(p.out)[o + i] = __float2bfloat16_rn(a[j]);
+                    else
+                        static_cast<float*>(p.out)[o + i] = a[j];
                 }
-                if constexpr (KC >= 0) {
-                    const float ref = rs[j].rebase(fmaxf(rs[j].m, a), p.c);
-                    rs[j].add(a, ref, p.c);
-                    if constexpr (KC > 0) wt[j].offer(a, (int)v, lane);
+            } else {
+                if (p.neg) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        a[j] = 32 * (slice + wpt * j) + lane < rows ? -a[j] : kNegInf;
+                }
+                float mx = rs[q].m;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) mx = fmaxf(mx, a[j]);
+                const float ref = rs[q].rebase(mx, p.c);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    rs[q].add(a[j], ref, p.c);
+                    if constexpr (KC > 0)
+                        wt[q].offer(a[j], (int)(v0 + 32 * (slice + wpt * j) + lane), lane);
                 }
             }
         }
@@ -511,8 +531,7 @@ k_few(const __grid_constant__ FewParams p) {
     if constexpr (KC >= 0) {
         // a warp's lanes, then a token's warps (through lg), become one part
         float* sm_stats = lg;                               // [warp][3]
-        float* sm_v = lg + 3 * Cfg::CONSUMERS;              // [warp][32]
-        int* sm_id = reinterpret_cast<int*>(sm_v + 32 * Cfg::CONSUMERS);
+        uint64_t* sm_key = reinterpret_cast<uint64_t*>(lg + 4 * Cfg::CONSUMERS);  // [warp][32]
 #pragma unroll
         for (int j = 0; j < Cfg::TPW; ++j) {
             const int tok = tok0 + j * Cfg::CONSUMERS;
@@ -534,10 +553,7 @@ k_few(const __grid_constant__ FewParams p) {
                     sm_stats[3 * warp + 1] = l;
                     sm_stats[3 * warp + 2] = w;
                 }
-                if (KC > 0) {
-                    sm_v[32 * warp + lane] = lane < KC ? wt[j].v : kNegInf;
-                    sm_id[32 * warp + lane] = wt[j].id;
-                }
+                if (KC > 0) sm_key[32 * warp + lane] = lane < KC ? wt[j].key : 0;
                 consumers_sync<32 * Cfg::CONSUMERS>();
                 if (!mine || slice != 0) continue;
                 float ml = kNegInf, ll = 0.f, wl = 0.f;     // lane i < wpt: the i-th warp's
@@ -564,19 +580,18 @@ k_few(const __grid_constant__ FewParams p) {
                 }
                 if constexpr (KC > 0)
                     for (int i = 1; i < wpt; ++i)
-                        wt[j].offer(sm_v[32 * (warp + i) + lane], sm_id[32 * (warp + i) + lane],
-                                    lane);
+                        wt[j].offer_key(sm_key[32 * (warp + i) + lane], lane);
             }
             if (!mine) continue;
             const size_t part = blockIdx.x;
             const int row = p.row0 + tok;
             int n = 0;
             if constexpr (KC > 0) {
-                const bool has = lane < KC && wt[j].v > kNegInf;
+                const bool has = lane < KC && wt[j].key != 0;
                 n = __popc(__ballot_sync(0xffffffffu, has));
                 if (has)
                     p.parts.top[(part * KC + lane) * p.parts.ld + row] =
-                        make_float2(wt[j].v, __int_as_float(wt[j].id));
+                        make_float2(rank_value(wt[j].key), __int_as_float(rank_id(wt[j].key)));
             }
             if (lane == 0)
                 p.parts.stats[part * p.parts.ld + row] = make_float4(mx, l, w, __int_as_float(n));

@@ -189,33 +189,63 @@ struct SimtLogprob {
     }
 };
 
+// (value, id) as one integer that is larger for what ranks first: the larger
+// value, then the lower id (0 to 2^31 - 1).  0 stands for nothing.
+__device__ __forceinline__ uint64_t rank_key(float v, int id) {
+    return (uint64_t)float_key(v) << 32 | (uint32_t)(0x7fffffff - id);
+}
+__device__ __forceinline__ float rank_value(uint64_t k) { return key_float((uint32_t)(k >> 32)); }
+__device__ __forceinline__ int rank_id(uint64_t k) { return 0x7fffffff - (int)(uint32_t)k; }
+
+// This lane and lane ^ d exchange: keep the larger key if `larger`.
+__device__ __forceinline__ uint64_t warp_exchange(uint64_t k, int d, bool larger) {
+    const uint64_t o = __shfl_xor_sync(0xffffffffu, k, d);
+    return (k > o) == larger ? k : o;
+}
+
+// The 32 best of a sorted list (lane j the j-th) and 32 offers, sorted: sort
+// the offers, best first; max(list[i], offers[31 - i]) are the 32 best, and a
+// bitonic sequence.  (Not inlined: it is used in unrolled loops.)
+__device__ __noinline__ uint64_t warp_merge_best(uint64_t list, uint64_t k, int lane) {
+#pragma unroll
+    for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+        for (int d = size >> 1; d > 0; d >>= 1)
+            k = warp_exchange(k, d, ((lane & size) == 0) == ((lane & d) == 0));
+    const uint64_t r = __shfl_sync(0xffffffffu, k, 31 - lane);
+    list = list > r ? list : r;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) list = warp_exchange(list, d, (lane & d) == 0);
+    return list;
+}
+
 // ======================================================================
-// Candidate list of one row held across a warp: lane j < KC has the j-th best.
+// Candidate list of one row held across a warp: lane j has the j-th best
+// key, of which the first KC count (0: none yet).
 // ======================================================================
 template <int KC>
 struct WarpTop {
-    float v = kNegInf;
-    int id = 0x7fffffff;
+    uint64_t key = 0;
 
-    static __device__ __forceinline__ bool better(float xv, int xi, float yv, int yi) {
-        return xv > yv || (xv == yv && xi < yi);
-    }
-    // Every lane offers one (x, col); x = -inf (or NaN) offers nothing.
+    // Every lane offers one (x, col); x = -inf (or NaN) offers nothing.  A few
+    // that enter are inserted one by one (about 100 cycles each); more are
+    // sorted, and merged with the list, by bitonic steps (about 700 cycles).
     __device__ __forceinline__ void offer(float x, int col, int lane) {
-        float kv = __shfl_sync(0xffffffffu, v, KC - 1);
-        int ki = __shfl_sync(0xffffffffu, id, KC - 1);
-        uint32_t mask = __ballot_sync(0xffffffffu, x > -CUDART_INF_F && better(x, col, kv, ki));
+        offer_key(x > kNegInf ? rank_key(x, col) : 0, lane);
+    }
+    __device__ __forceinline__ void offer_key(uint64_t k, int lane) {
+        uint32_t mask = __ballot_sync(0xffffffffu, k > __shfl_sync(0xffffffffu, key, KC - 1));
+        if (__popc(mask) > 6) {
+            key = warp_merge_best(key, k, lane);
+            return;
+        }
         while (mask != 0) {
             const int src = __ffs(mask) - 1;
             mask &= mask - 1;
-            const float xv = __shfl_sync(0xffffffffu, x, src);
-            const int xi = __shfl_sync(0xffffffffu, col, src);
-            const uint32_t ahead = __ballot_sync(0xffffffffu, lane < KC && better(v, id, xv, xi));
-            const int pos = __popc(ahead);         // the list is sorted: a prefix of lanes
-            const float pv = __shfl_up_sync(0xffffffffu, v, 1);
-            const int pi = __shfl_up_sync(0xffffffffu, id, 1);
-            if (lane > pos) { v = pv; id = pi; }
-            if (lane == pos) { v = xv; id = xi; }
+            const uint64_t x1 = __shfl_sync(0xffffffffu, k, src);
+            const int pos = __popc(__ballot_sync(0xffffffffu, key > x1));   // a prefix of lanes
+            const uint64_t up = __shfl_up_sync(0xffffffffu, key, 1);
+            key = lane > pos ? up : (lane == pos ? x1 : key);
         }
     }
 };
@@ -348,14 +378,6 @@ struct LpMergeParams {
 };
 
 constexpr int kMergeKeep = 6;        // slices a thread keeps in registers
-
-// (value, id) as one integer that is larger for what ranks first: the larger
-// value, then the lower id (0 to 2^31 - 1).  0 stands for nothing.
-__device__ __forceinline__ uint64_t rank_key(float v, int id) {
-    return (uint64_t)float_key(v) << 32 | (uint32_t)(0x7fffffff - id);
-}
-__device__ __forceinline__ float rank_value(uint64_t k) { return key_float((uint32_t)(k >> 32)); }
-__device__ __forceinline__ int rank_id(uint64_t k) { return 0x7fffffff - (int)(uint32_t)k; }
 
 __device__ __forceinline__ uint64_t warp_max(uint64_t k) {
     const uint32_t hi = (uint32_t)(k >> 32);
