@@ -422,7 +422,7 @@ int fldce_logprob(fldce_handle h, const fldce_logprob_call* call);
  *                       dlogprob holds at ignored tokens is not read.
  *   dH, dW, db          [device, out] as for fldce_fwd_bwd_ex; each may be
  *                       NULL when it is not needed (one has to be set).
- *   workspace           at least fldce_workspace_size(h, N) bytes.
+ *   workspace           at least fldce_logprob_bwd_workspace_size(h, N) bytes.
  *   err_count, stream   as above.
  * N == 0 writes dW = 0 and db = 0 (nothing with DW_ACCUMULATE).
  * Errors: INVALID_ARG, UNSUPPORTED, ALIGN, WORKSPACE, DEVICE, CUDA.
@@ -447,6 +447,10 @@ typedef struct {
 } fldce_logprob_grad_call;
 
 int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* call);
+
+/* fldce_logprob_bwd_workspace_size -- workspace bytes of fldce_logprob_bwd.
+ * Errors: INVALID_ARG, UNSUPPORTED (plan). */
+int fldce_logprob_bwd_workspace_size(fldce_handle h, int64_t N, size_t* bytes);
 
 /*
  * 4-bit head weight: W[v, d] = q[v, d] * scale[v, d / group] with q a two's

@@ -40,7 +40,8 @@ EXPORTS = ("fldce_create", "fldce_workspace_size", "fldce_chunk_size", "fldce_fw
            "fldce_fwd_bwd_noalloc", "fldce_forward", "fldce_fwd_bwd_ex", "fldce_forward_ex",
            "fldce_count_valid", "fldce_vp_stats", "fldce_vp_fwd_bwd",
            "fldce_profile_begin", "fldce_profile_end", "fldce_profile_kind_name",
-           "fldce_logprob_workspace_size", "fldce_logprob", "fldce_logprob_bwd",
+           "fldce_logprob_workspace_size", "fldce_logprob", "fldce_logprob_bwd_workspace_size",
+           "fldce_logprob_bwd",
            "fldce_w4_quantize", "fldce_w4_linear",
            "fldce_scale", "fldce_selftest_wait", "fldce_destroy", "fldce_strerror", "fldce_version")
 FLDCE_PROF_KINDS = 9
@@ -190,6 +191,8 @@ def load() -> ctypes.CDLL:
     lib.fldce_logprob_workspace_size.argtypes = [_P, _I64, ctypes.c_int32,
                                                  ctypes.POINTER(ctypes.c_size_t)]
     lib.fldce_logprob_workspace_size.restype = ctypes.c_int
+    lib.fldce_logprob_bwd_workspace_size.argtypes = [_P, _I64, ctypes.POINTER(ctypes.c_size_t)]
+    lib.fldce_logprob_bwd_workspace_size.restype = ctypes.c_int
     lib.fldce_logprob.argtypes = [_P, ctypes.POINTER(fldce_logprob_call)]
     lib.fldce_logprob.restype = ctypes.c_int
     lib.fldce_logprob_bwd.argtypes = [_P, ctypes.POINTER(fldce_logprob_grad_call)]
@@ -380,6 +383,13 @@ def fldce_logprob_workspace_size(h, N: int, top_k: int) -> int:
     ws = ctypes.c_size_t()
     _check(load().fldce_logprob_workspace_size(h, int(N), int(top_k), ctypes.byref(ws)),
            "fldce_logprob_workspace_size")
+    return ws.value
+
+
+def fldce_logprob_bwd_workspace_size(h, N: int) -> int:
+    ws = ctypes.c_size_t()
+    _check(load().fldce_logprob_bwd_workspace_size(h, int(N), ctypes.byref(ws)),
+           "fldce_logprob_bwd_workspace_size")
     return ws.value
 
 

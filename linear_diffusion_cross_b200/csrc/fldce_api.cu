@@ -144,15 +144,24 @@ bool make_store_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t ro
     return make_map(m, base, cols, rows, ld, elt == 4 ? 32 : 64, 32, elt);
 }
 
+// The store map of `p` and the plain view of the same matrix.
+bool set_store(StoreEpi::Params* p, int mode, void* base, int64_t cols, int64_t rows, int elt) {
+    p->mode = mode;
+    p->out = base;
+    p->rows = rows;
+    p->cols = cols;
+    return make_store_map(&p->omap, base, cols, rows, cols, elt);
+}
+
 // K splits of a GEMM with `tiles` output tiles and `k_iters` K steps on
 // `pairs` CTA pairs.  The persistent schedule runs ceil(k tiles / pairs)
 // rounds of ceil(k_iters / k) steps; a split is taken only when it shortens
 // that by more than 2% (each split costs an fp32 partial buffer and its
 // share of the fixed-order sum) and keeps >= 16 K steps per split.
-int choose_k_splits(int64_t tiles, int64_t k_iters, int pairs) {
+int choose_k_splits(int64_t tiles, int64_t k_iters, int pairs, int max_splits) {
     auto cost = [&](int64_t k) { return cdiv(k * tiles, pairs) * cdiv(k_iters, k); };
     int best = 1;
-    for (int k = 2; k <= kMaxKSplits; ++k)
+    for (int k = 2; k <= max_splits; ++k)
         if (k_iters >= 16 * k && (double)cost(k) < 0.98 * (double)cost(best)) best = k;
     return best;
 }
@@ -185,18 +194,18 @@ struct DhPlan {
     int k_splits;
 };
 
-DhPlan plan_dh(int64_t rows, int64_t D, int64_t V, int pairs) {
+DhPlan plan_dh(int64_t rows, int64_t D, int64_t V, int pairs, int max_splits) {
     const int64_t k_iters = cdiv(V, 64);
     const int64_t mt = cdiv(rows, 256);
     auto cost = [&](int64_t tiles, int ks) {
         return (double)(cdiv(ks * tiles, pairs) * cdiv(k_iters, ks));
     };
     const int64_t nt = mt * cdiv(D, 256);
-    const int kn = choose_k_splits(nt, k_iters, pairs);
+    const int kn = choose_k_splits(nt, k_iters, pairs, max_splits);
     DhPlan p{false, kn};
     if (round_up((size_t)D, 512) * 10 > round_up((size_t)D, 256) * 11) return p;
     const int64_t wt = mt * cdiv(D, 512);
-    const int kw = choose_k_splits(wt, k_iters, pairs);
+    const int kw = choose_k_splits(wt, k_iters, pairs, max_splits);
     if (2.0 * kWideDhCost * cost(wt, kw) < cost(nt, kn)) p = DhPlan{true, kw};
     return p;
 }
@@ -485,6 +494,7 @@ struct GradGemm {
     int rows;
     int64_t r0;               // first token of the chunk
     DynRows dyn;              // compacted rows (dim is set per product)
+    int max_splits = kMaxKSplits;   // K splits of dH that L->dh_acc has room for
 
     // dH = G W (K = V).  When one pass over the tiles leaves many SMs
     // idle in its last round, the vocabulary is split into k ranges;
@@ -492,7 +502,7 @@ struct GradGemm {
     // sums them in split order (deterministic) into dH.
     int dh(const CUtensorMap& mG_k, const CUtensorMap& mW_mn, void* dH) const {
         const int64_t D = h->cfg.D, V = h->cfg.V;
-        const DhPlan dp = plan_dh(rows, D, V, std::max(1, dev->sms / 2));
+        const DhPlan dp = plan_dh(rows, D, V, std::max(1, dev->sms / 2), max_splits);
         const int ks = dp.k_splits;
         StoreEpi::Params hp;
         const bool dh_fp32 = (h->cfg.flags & FLDCE_FLAG_DH_FP32) != 0;
@@ -500,16 +510,13 @@ struct GradGemm {
         const int split_rows = (int)round_up((size_t)rows, 256);
         void* dHc = static_cast<uint8_t*>(dH) + (size_t)r0 * D * (dh_fp32 ? 4 : 2);
         if (ks > 1) {
-            if (!make_store_map(&hp.omap, part, D, (uint64_t)ks * split_rows, D, 4))
+            if (!set_store(&hp, WS_STORE, part, D, (int64_t)ks * split_rows, 4))
                 return FLDCE_ERR_CUDA;
-            hp.mode = WS_STORE;
             hp.split_rows = split_rows;
         } else if (dh_fp32) {
-            if (!make_store_map(&hp.omap, dHc, D, rows, D, 4)) return FLDCE_ERR_CUDA;
-            hp.mode = WS_STORE;
+            if (!set_store(&hp, WS_STORE, dHc, D, rows, 4)) return FLDCE_ERR_CUDA;
         } else {
-            if (!make_store_map(&hp.omap, dHc, D, rows, D, 2)) return FLDCE_ERR_CUDA;
-            hp.mode = OUT_BF16;
+            if (!set_store(&hp, OUT_BF16, dHc, D, rows, 2)) return FLDCE_ERR_CUDA;
         }
         const Walk dh_walk{1, ks, kOneBlock};
         const DynRows dr{dyn.count, dyn.base, 1};
@@ -536,13 +543,12 @@ struct GradGemm {
         float* dw_ws = fp32_dw ? static_cast<float*>(dW) : reinterpret_cast<float*>(ws + L->dw_acc);
         StoreEpi::Params wp;
         if (L->nchunks == 1 && !fp32_dw && !accum) {
-            if (!make_store_map(&wp.omap, dW, D, V, D, 2)) return FLDCE_ERR_CUDA;
-            wp.mode = OUT_BF16;
+            if (!set_store(&wp, OUT_BF16, dW, D, V, 2)) return FLDCE_ERR_CUDA;
         } else {
             // fp32 partial sums; an fp32 dW accumulated into takes
             // every chunk's reduce-add directly
-            if (!make_store_map(&wp.omap, dw_ws, D, V, D, 4)) return FLDCE_ERR_CUDA;
-            wp.mode = (ci == 0 && !(accum && fp32_dw)) ? WS_STORE : WS_ADD;
+            const int mode = (ci == 0 && !(accum && fp32_dw)) ? WS_STORE : WS_ADD;
+            if (!set_store(&wp, mode, dw_ws, D, V, 4)) return FLDCE_ERR_CUDA;
         }
         const Walk dw_walk{1, 1, kOneBlock};
         FLDCE_CUDA((launch_gemm<CfgMM, StoreEpi>(mG_mn, mH_mn, (int)V, D, rows, dw_walk, wp,

@@ -351,6 +351,11 @@ struct GEpi {
 // A GEMM split over K (dH over vocabulary ranges) stores split j's tile
 // split_rows * j rows further down, so every split owns a partial buffer
 // that a later pass sums in a fixed order.
+//
+// A 32-row box that hangs over the last row is written by its lanes instead
+// (one row each): a TMA store takes 0.7 us for every row outside the map
+// (measured: G of 6 rows, 957 us against 294 us for 32 rows), which is the
+// tail of the whole product when the vocabulary is no multiple of 32.
 // ======================================================================
 enum StoreMode { OUT_BF16 = 0, WS_STORE = 1, WS_ADD = 2 };
 
@@ -359,7 +364,37 @@ struct StoreEpi {
         CUtensorMap omap;        // bf16 [rows, cols] box 64 x 32, or fp32 box 32 x 32
         int mode;
         int split_rows = 0;      // row offset between K splits' partial buffers
+        void* out = nullptr;     // the map's matrix: rows x cols, rows `cols` apart
+        int64_t rows = 0;
+        int64_t cols = 0;
     };
+
+    // Columns [c0, c0 + 32) of row `row` from this lane's accumulator row.
+    static __device__ __forceinline__ void put_row(const Params& p, int64_t row, int64_t c0,
+                                                   const uint32_t (&r)[32]) {
+        if (row >= p.rows) return;
+        if (p.mode == OUT_BF16) {
+            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + row * p.cols + c0;
+            float v[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint4 a, b;
+                pack16(v + 16 * h, a, b);
+                if (c0 + 16 * h + 8 <= p.cols) reinterpret_cast<uint4*>(o)[2 * h] = a;
+                if (c0 + 16 * h + 16 <= p.cols) reinterpret_cast<uint4*>(o)[2 * h + 1] = b;
+            }
+        } else {
+            float* o = static_cast<float*>(p.out) + row * p.cols + c0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                if (c0 + i >= p.cols) break;
+                if (p.mode == WS_ADD) atomicAdd(o + i, __uint_as_float(r[i]));
+                else o[i] = __uint_as_float(r[i]);
+            }
+        }
+    }
 
     template <class Cfg>
     static __device__ __forceinline__ void run(const Params& p, const TileCtx& t,
@@ -367,8 +402,11 @@ struct StoreEpi {
         const int64_t n0 = t.col0;
         const int y = t.row0 + t.split * p.split_rows + 32 * t.q;
         const int mode = p.mode;
+        const bool hangs_over = y + 32 > p.rows;       // the same for the whole warp
         for_each_chunk<Cfg::NCHUNK>(acc, [&](const uint32_t (&r)[32], int j) {
-            if (mode == OUT_BF16) {
+            if (hangs_over) {
+                put_row(p, y + t.lane, n0 + 32 * j, r);
+            } else if (mode == OUT_BF16) {
                 float v[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);

@@ -46,6 +46,40 @@ LpLayout lp_layout(const fldce_plan* p, int64_t N, int top_k, bool w4) {
     return L;
 }
 
+// Workspace of the gradient.  G has room for whole 32-row store boxes; dH of
+// few tokens, whose products have few tiles, may be split over K more often
+// than the loss's (16 partials of up to 256 rows are small).
+constexpr int kLpFewRowsSplits = 16;
+int lp_max_splits(int64_t C) { return C <= 256 ? kLpFewRowsSplits : kMaxKSplits; }
+
+Layout lp_bwd_layout(const fldce_plan* p, int64_t N) {
+    Layout L{};
+    const int64_t C = std::max<int64_t>(1, std::min<int64_t>(p->chunk, N));
+    L.C = C;
+    L.nchunks = N > 0 ? cdiv(N, p->chunk) : 0;
+    const bool bf16 = p->cfg.dtype == FLDCE_BF16;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = off;
+        off = round_up(off + bytes, kAlign);
+        return o;
+    };
+    L.cnt = take(sizeof(Counters));
+    L.zy = take(C * 4);
+    L.row_lse2 = take(C * 4);
+    L.row_gcoef = take(C * 4);
+    L.row_y = take(C * 4);
+    L.loss_tok = take(C * 4);
+    L.G = take(round_up((size_t)C, 32) * p->Vpad * p->elt);
+    L.dh_acc = take(bf16 ? (size_t)lp_max_splits(C) * round_up((size_t)C, 256) * p->cfg.D * 4 : 0);
+    const bool acc = (L.nchunks > 1 || (dw_accumulate(p) && N > 0)) && !dw_out_fp32(p);
+    L.dw_acc = take(acc ? (size_t)p->cfg.V * p->cfg.D * 4 : 0);
+    L.db_part = take((size_t)kColsumSegs * p->cfg.V * 4);
+    L.db_acc = take((size_t)p->cfg.V * 4);
+    L.total = off;
+    return L;
+}
+
 // Shapes every 4-bit weight has to have.
 int check_w4(const void* packed, const void* scales, int group, int64_t V, int64_t D) {
     if (V <= 0 || D <= 0) return FLDCE_ERR_INVALID_ARG;
@@ -313,6 +347,13 @@ int fldce_logprob(fldce_handle h, const fldce_logprob_call* cp) {
     }
 }
 
+int fldce_logprob_bwd_workspace_size(fldce_handle h, int64_t N, size_t* bytes) {
+    if (h == nullptr || bytes == nullptr || N < 0 || N > h->cfg.max_N) return FLDCE_ERR_INVALID_ARG;
+    if (int e = check_lp_plan(h)) return e;
+    *bytes = lp_bwd_layout(h, N).total;
+    return FLDCE_OK;
+}
+
 int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
     if (h == nullptr || cp == nullptr) return FLDCE_ERR_INVALID_ARG;
     const fldce_logprob_grad_call& c = *cp;
@@ -332,7 +373,7 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
     if (!aligned_to(c.token, 8) || !aligned_to(c.lse, 4) || !aligned_to(c.entropy, 4) ||
         !aligned_to(c.dlogprob, 4) || !aligned_to(c.dentropy, 4) || !aligned_to(c.err_count, 4))
         return FLDCE_ERR_ALIGN;
-    const Layout L = make_layout(h, N);
+    const Layout L = lp_bwd_layout(h, N);
     if (c.workspace_bytes < L.total) return FLDCE_ERR_WORKSPACE;
     DeviceInfo dev;
     if (int s = check_device(&dev)) return s;
@@ -378,7 +419,8 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
         if (bf16) {
             CUtensorMap mH_k, mH_mn, mG_k, mG_mn;
             LogprobGEpi::Params gp;
-            if (!make_store_map(&gp.gmap, G, V, rows, h->Vpad, 2) ||
+            // (whole boxes of rows: rows past the tokens get zeros)
+            if (!make_store_map(&gp.gmap, G, V, round_up((size_t)rows, 32), h->Vpad, 2) ||
                 !make_map(&mH_k, Hc, D, rows, D, 64, 128) ||
                 !make_map(&mH_mn, Hc, D, rows, D, 64, 64) ||
                 !make_map(&mG_k, G, V, rows, h->Vpad, 64, 128) ||
@@ -394,7 +436,8 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
             FLDCE_CUDA((launch_gemm<CfgKK, LogprobGEpi>(mH_k, mW_k, rows, V, D, walk, gp,
                                                         &cnt->dev_err, dev.sms, st)));
             prof_mark(h, PK_G, st);
-            const GradGemm gg{h, &L, ws, cnt, &dev, st, rows, r0, DynRows()};
+            const GradGemm gg{h,  &L,   ws, cnt,       &dev,
+                              st, rows, r0, DynRows(), lp_max_splits(L.C)};
             if (c.dH != nullptr)
                 if (int e = gg.dh(mG_k, mW_mn, c.dH)) return e;
             if (c.dW != nullptr)

@@ -115,7 +115,7 @@ class FusedLinearLogProbsFunction(torch.autograd.Function):
             dH = torch.empty_like(x) if need_x else None
             dW = torch.empty_like(weight) if need_w else None
             db = torch.empty_like(bias) if need_b else None
-            nbytes = B.fldce_workspace_size(ctx.h, N)
+            nbytes = B.fldce_logprob_bwd_workspace_size(ctx.h, N)
             ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
             call = B.make_logprob_grad_call(
                 H=x, W=weight, bias=bias, token=token, N=N, lse=lse, entropy=entropy,

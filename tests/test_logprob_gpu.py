@@ -409,7 +409,8 @@ def test_c_gradient_flags(flags, chunk):
     x, y, w, b = make(N, D, V, BF, bias=True)
     a, e = torch.randn(N, device=DEV), torch.randn(N, device=DEV)
     r = fused_linear_logprobs(x, y, w, b)
-    h, ws_bytes = B.fldce_create(B.FLDCE_BF16, D, V, N, chunk_N=chunk, flags=flags)
+    h, _ = B.fldce_create(B.FLDCE_BF16, D, V, N, chunk_N=chunk, flags=flags)
+    ws_bytes = B.fldce_logprob_bwd_workspace_size(h, N)
     ws = torch.empty(ws_bytes, dtype=torch.uint8, device=DEV)
     dwt = F32 if flags & B.FLDCE_FLAG_DW_FP32 else BF
     dht = F32 if flags & B.FLDCE_FLAG_DH_FP32 else BF
@@ -440,7 +441,7 @@ def test_captured_graphs_and_streams(N):
     def step(xx):
         r = fused_linear_logprobs(xx, y, w, b, top_k=3)
         dH, dW = torch.empty_like(xx), torch.empty_like(w)
-        nb = B.fldce_workspace_size(h, N)
+        nb = B.fldce_logprob_bwd_workspace_size(h, N)
         ws = torch.empty(nb, dtype=torch.uint8, device=DEV)
         B.fldce_logprob_bwd(h, B.make_logprob_grad_call(
             H=xx, W=w, bias=b, token=y, N=N, lse=r.lse, entropy=r.entropy, dlogprob=a, dentropy=e,
@@ -496,7 +497,7 @@ def test_first_cuda_call_of_a_thread(N):
     a, e = torch.randn(N, device=DEV), torch.randn(N, device=DEV)
     ref, rref = grads_of(x, y, w, b, 1.0, a, e, top_k=3)
     h, _ = B.fldce_create(B.FLDCE_BF16, 128, 3000, N)
-    nb = B.fldce_workspace_size(h, N)
+    nb = B.fldce_logprob_bwd_workspace_size(h, N)
     ws = torch.empty(max(nb, B.fldce_logprob_workspace_size(h, N, 0)), dtype=torch.uint8, device=DEV)
     dH, lse, ent = torch.zeros_like(x), torch.zeros(N, device=DEV), torch.zeros(N, device=DEV)
     torch.cuda.synchronize()
