@@ -472,14 +472,16 @@ int fldce_w4_quantize(const void* W, int32_t dtype, int64_t V, int64_t D, int32_
  * fldce_w4_linear -- logits of a few tokens: out[n, v] = <x[n], W[v]> (+
  * bias[v]), summed in fp32 and rounded once to out_dtype.
  *   x [device, in] [N, D] bf16, 16-byte aligned; bias [V] bf16 or NULL;
- *   out [device, out] [N, V] of out_dtype (FLDCE_BF16 or FLDCE_FP32).
+ *   out [device, out] [N, V] of out_dtype (FLDCE_BF16 or FLDCE_FP32);
+ *   err_count [device, out, may be NULL] 2 int32: [0] = 0, [1] = device error
+ *   bits as for fldce_fwd_bwd.
  * The weight is read once for every few tokens; with many tokens a 16-bit
  * weight and a dense product are faster.
  * Errors: INVALID_ARG, UNSUPPORTED, ALIGN, DEVICE, CUDA.
  */
 int fldce_w4_linear(const void* x, int64_t N, const void* packed, const void* scales, int32_t group,
                     const void* bias, int64_t V, int64_t D, void* out, int32_t out_dtype,
-                    void* stream);
+                    int32_t* err_count, void* stream);
 
 /*
  * Optional profiling window: per-kernel device time over a window of calls.

@@ -200,7 +200,7 @@ def load() -> ctypes.CDLL:
     lib.fldce_w4_quantize.argtypes = [_P, ctypes.c_int32, _I64, _I64, ctypes.c_int32, _P, _P, _P]
     lib.fldce_w4_quantize.restype = ctypes.c_int
     lib.fldce_w4_linear.argtypes = [_P, _I64, _P, _P, ctypes.c_int32, _P, _I64, _I64, _P,
-                                    ctypes.c_int32, _P]
+                                    ctypes.c_int32, _P, _P]
     lib.fldce_w4_linear.restype = ctypes.c_int
     lib.fldce_selftest_wait.argtypes = [_I64, _P, _P]
     lib.fldce_selftest_wait.restype = ctypes.c_int
@@ -407,10 +407,11 @@ def fldce_w4_quantize(W, dtype, V, D, group, packed, scales, stream=None) -> int
                   "fldce_w4_quantize")
 
 
-def fldce_w4_linear(x, N, packed, scales, group, bias, V, D, out, out_dtype, stream=None) -> int:
+def fldce_w4_linear(x, N, packed, scales, group, bias, V, D, out, out_dtype, err_count=None,
+                    stream=None) -> int:
     return _check(load().fldce_w4_linear(_ptr(x), int(N), _ptr(packed), _ptr(scales), int(group),
                                          _ptr(bias), int(V), int(D), _ptr(out), int(out_dtype),
-                                         _stream(stream)), "fldce_w4_linear")
+                                         _ptr(err_count), _stream(stream)), "fldce_w4_linear")
 
 
 def fldce_scale(x, n, dtype, g, stream=None) -> int:

@@ -79,10 +79,13 @@ struct FewParams {
     int neg;                   // s < 0
     LpParts parts;             // rows row0 .. row0 + n_tok - 1
     int row0;
-    // logits
-    void* out;                 // [n_tok][V]
+    // logits, or their gradient
+    void* out;                 // [n_tok][V] (gradient: bf16, rows ldo apart)
     int out_bf16;
-    int32_t* err;
+    int64_t ldo;
+    float c2;                  // s log2(e)
+    LpCoef k;                  // the gradient's row coefficients
+    int32_t* err;              // device error bits, or null
 };
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* m, uint32_t bar,
@@ -190,7 +193,10 @@ __device__ __forceinline__ void consumers_sync() {
     asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
 }
 
-// KC >= 0: statistics and KC candidates per (CTA, token).  KC < 0: logits.
+// KC >= 0: statistics and KC candidates per (CTA, token).  -1: logits.
+// -2: the logits' gradient (as LogprobGEpi, for few tokens: that kernel's
+// 256-row tiles of H, nearly empty, make every SM read the same few lines of
+// L2 at a time: 957 us for 6 tokens of 3920 x 159722, 215 us here).
 // LB: log2 of a 4-bit weight's group in 32-element blocks.
 template <bool W4, int LB, int NT, int KC>
 __global__ void __launch_bounds__(FewCfg<W4, LB, NT>::THREADS, 1)
@@ -285,7 +291,7 @@ k_few(const __grid_constant__ FewParams p) {
             }
         }
         if (!ok) {
-            if (lane == 0) atomicOr(p.err, FLDCE_DEV_ERR_TIMEOUT);
+            if (lane == 0 && p.err != nullptr) atomicOr(p.err, FLDCE_DEV_ERR_TIMEOUT);
             // loads in flight land before the CTA may exit (bounded again)
             for (int i = it > S ? it - S : 0; i < it; ++i)
                 mbar_wait_bounded(full_bar(i % S), (i / S) & 1u, kWaitLimitNs);
@@ -344,7 +350,7 @@ k_few(const __grid_constant__ FewParams p) {
         for (int k = 0; k < p.k_stages; ++k) {
                 if (ok && !mbar_wait_bounded(full_bar(s), ph, kWaitLimitNs)) {
                     ok = false;
-                    if (lane == 0) atomicOr(p.err, FLDCE_DEV_ERR_TIMEOUT);
+                    if (lane == 0 && p.err != nullptr) atomicOr(p.err, FLDCE_DEV_ERR_TIMEOUT);
                 }
                 if (!ok) continue;
             if (active) {
@@ -497,7 +503,21 @@ k_few(const __grid_constant__ FewParams p) {
                 const int i = 32 * (slice + wpt * j) + lane;
                 a[j] = i < rows ? src[i] + bias[j] : kNegInf;
             }
-            if constexpr (KC < 0) {
+            if constexpr (KC == -2) {
+                const float L2 = p.k.lse2[tok], kap = p.k.kap[tok], ee = p.k.ee[tok];
+                const float ta = p.k.ta[tok];
+                const int64_t y = p.k.y[tok];
+                const bool dead = kap == 0.f && ee == 0.f && ta == 0.f;
+                __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + (int64_t)tok * p.ldo + v0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int i = 32 * (slice + wpt * j) + lane;
+                    if (i >= rows) continue;
+                    float gr = lp_grad(fmaf(a[j], p.c2, -L2), kap, ee);
+                    if (v0 + i == y) gr += ta;
+                    o[i] = __float2bfloat16_rn(dead ? 0.f : gr);
+                }
+            } else if constexpr (KC < 0) {
                 const int64_t o = (int64_t)tok * p.V + v0;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {

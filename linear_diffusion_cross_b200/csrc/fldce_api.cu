@@ -300,8 +300,9 @@ cudaError_t launch_fused_gdh(const CUtensorMap& mH, const CUtensorMap& mW, const
 // db (+)= column sums of the chunk's G, in a fixed order (two passes).
 cudaError_t launch_colsum(const void* G, bool g_bf16, int64_t ldg, int rows, int64_t V,
                           float* part, float* acc, bool add, cudaStream_t st,
-                          const int32_t* dyn_count = nullptr, int dyn_base = 0) {
-    const int nseg = (int)std::min<int64_t>(kColsumSegs, std::max<int64_t>(1, cdiv(rows, 256)));
+                          const int32_t* dyn_count = nullptr, int dyn_base = 0,
+                          int seg_min = 256) {
+    const int nseg = (int)std::min<int64_t>(kColsumSegs, std::max<int64_t>(1, cdiv(rows, seg_min)));
     const int seg_rows = (int)cdiv(rows, nseg);
     const dim3 grid((unsigned)cdiv(cdiv(V, 2), 128), (unsigned)nseg);
     if (g_bf16)

@@ -1018,6 +1018,8 @@ __global__ void k_colsum_partial(const T* __restrict__ G, int64_t ldg, int rows,
     const int r0 = blockIdx.y * seg_rows;
     const int r1 = min(rows, r0 + seg_rows);
     float a0 = 0.f, a1 = 0.f;
+    // 16 rows' loads in flight; the sum stays in row order
+#pragma unroll 16
     for (int r = r0; r < r1; ++r) {
         const T* row = G + (size_t)r * ldg + v;
         if constexpr (sizeof(T) == 2) {
@@ -1155,15 +1157,40 @@ simt_gemm_kernel(const float* __restrict__ A, int64_t sam, int64_t sak,
     const int64_t n0 = (int64_t)blockIdx.x * kSimtTile;
     const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
     float acc[4][4] = {};
-    for (int k0 = 0; k0 < K; k0 += 16) {
-        for (int e = threadIdx.x; e < 16 * kSimtTile; e += 256) {
-            const int mm = e % kSimtTile, kk = e / kSimtTile;
-            const int gm = m0 + mm, gk = k0 + kk;
-            As[kk][mm] = (gm < M && gk < K) ? A[(int64_t)gm * sam + (int64_t)gk * sak] : 0.f;
+    // Element i of this thread's four of an operand tile: consecutive threads
+    // along K where that is contiguous, else along the other dimension.  The
+    // next tile's elements are loaded while the current one is multiplied.
+    float ra[4], rb[4];
+    auto at = [&](bool k_fast, int i, int& mm, int& kk) {
+        const int e = threadIdx.x + 256 * i;
+        mm = k_fast ? e / 16 : e % kSimtTile;
+        kk = k_fast ? e % 16 : e / kSimtTile;
+    };
+    auto load = [&](int k0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            int mm, kk;
+            at(sak == 1, i, mm, kk);
+            const int gm = m0 + mm, ga = k0 + kk;
+            ra[i] = (gm < M && ga < K) ? A[(int64_t)gm * sam + (int64_t)ga * sak] : 0.f;
+            at(sbk == 1, i, mm, kk);
             const int64_t gn = n0 + mm;
-            Bs[kk][mm] = (gn < N && gk < K) ? B[gn * sbn + (int64_t)gk * sbk] : 0.f;
+            const int gb = k0 + kk;
+            rb[i] = (gn < N && gb < K) ? B[gn * sbn + (int64_t)gb * sbk] : 0.f;
+        }
+    };
+    load(0);
+    for (int k0 = 0; k0 < K; k0 += 16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            int mm, kk;
+            at(sak == 1, i, mm, kk);
+            As[kk][mm] = ra[i];
+            at(sbk == 1, i, mm, kk);
+            Bs[kk][mm] = rb[i];
         }
         __syncthreads();
+        if (k0 + 16 < K) load(k0 + 16);
 #pragma unroll
         for (int kk = 0; kk < 16; ++kk) {
             float a[4], b[4];

@@ -431,10 +431,25 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
             gp.rows = rows;
             gp.k = k;
             gp.bias = static_cast<const __nv_bfloat16*>(c.bias);
-            const Walk walk{0, 1, walk_group(cdiv(rows, CfgKK::PAIR_M),
-                                             (size_t)CfgKK::PAIR_M * D * 2, kL2BudgetSweep)};
-            FLDCE_CUDA((launch_gemm<CfgKK, LogprobGEpi>(mH_k, mW_k, rows, V, D, walk, gp,
-                                                        &cnt->dev_err, dev.sms, st)));
+            if (rows <= kFewTokens) {
+                FewParams fp{};
+                fp.V = V;
+                fp.bias = gp.bias;
+                fp.n_tok = rows;
+                fp.out = G;
+                fp.ldo = h->Vpad;
+                fp.c2 = c2;
+                fp.k = k;
+                fp.err = &cnt->dev_err;
+                FLDCE_CUDA((launch_few<false, -2>(fp, HeadWeight{c.W, nullptr, 0, 0},
+                                                  reinterpret_cast<const __nv_bfloat16*>(Hc), D,
+                                                  dev.sms, st)));
+            } else {
+                const Walk walk{0, 1, walk_group(cdiv(rows, CfgKK::PAIR_M),
+                                                 (size_t)CfgKK::PAIR_M * D * 2, kL2BudgetSweep)};
+                FLDCE_CUDA((launch_gemm<CfgKK, LogprobGEpi>(mH_k, mW_k, rows, V, D, walk, gp,
+                                                            &cnt->dev_err, dev.sms, st)));
+            }
             prof_mark(h, PK_G, st);
             const GradGemm gg{h,  &L,   ws, cnt,       &dev,
                               st, rows, r0, DynRows(), lp_max_splits(L.C)};
@@ -463,7 +478,8 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
             }
         }
         if (c.db != nullptr) {
-            FLDCE_CUDA(launch_colsum(G, bf16, h->Vpad, rows, V, db_part, db_acc, ci > 0, st));
+            FLDCE_CUDA(launch_colsum(G, bf16, h->Vpad, rows, V, db_part, db_acc, ci > 0, st,
+                                     nullptr, 0, 32));
             if (ci + 1 == L.nchunks) {
                 k_cast_out<<<(unsigned)cdiv(V, 256), 256, 0, st>>>(
                     db_acc, c.db, V, dw_out_fp32(h) ? 0 : 1, accum ? 1 : 0);
@@ -500,24 +516,25 @@ int fldce_w4_quantize(const void* W, int32_t dtype, int64_t V, int64_t D, int32_
 
 int fldce_w4_linear(const void* x, int64_t N, const void* packed, const void* scales, int32_t group,
                     const void* bias, int64_t V, int64_t D, void* out, int32_t out_dtype,
-                    void* stream) {
+                    int32_t* err_count, void* stream) {
     if (N < 0 || N > (int64_t(1) << 31) - 1) return FLDCE_ERR_INVALID_ARG;
     if (out_dtype != FLDCE_BF16 && out_dtype != FLDCE_FP32) return FLDCE_ERR_UNSUPPORTED;
     if (int e = check_w4(packed, scales, group, V, D)) return e;
-    if (N == 0) return FLDCE_OK;
-    if (x == nullptr || out == nullptr) return FLDCE_ERR_INVALID_ARG;
-    if (!aligned16(x) || !aligned_to(bias, 2) ||
+    if (N > 0 && (x == nullptr || out == nullptr)) return FLDCE_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned_to(bias, 2) || !aligned_to(err_count, 4) ||
         !aligned_to(out, out_dtype == FLDCE_BF16 ? 2 : 4))
         return FLDCE_ERR_ALIGN;
     DeviceInfo dev;
     if (int s = check_device(&dev)) return s;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (err_count != nullptr) FLDCE_CUDA(cudaMemsetAsync(err_count, 0, 8, st));
     const HeadWeight hw = w4_weight(packed, scales, group, D);
     const size_t row_bytes = (size_t)V * (out_dtype == FLDCE_BF16 ? 2 : 4);
     FewParams fp{};
     fp.V = V;
     fp.bias = static_cast<const __nv_bfloat16*>(bias);
     fp.out_bf16 = out_dtype == FLDCE_BF16 ? 1 : 0;
+    fp.err = err_count != nullptr ? err_count + 1 : nullptr;
     for (int64_t t0 = 0; t0 < N; t0 += kFewTokens) {
         fp.n_tok = (int)std::min<int64_t>(kFewTokens, N - t0);
         fp.out = static_cast<uint8_t*>(out) + t0 * row_bytes;

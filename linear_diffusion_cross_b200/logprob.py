@@ -54,8 +54,14 @@ def _workspace_size(h: int, N: int, top_k: int) -> int:
     return B.fldce_logprob_workspace_size(h, N, top_k)
 
 
+@functools.lru_cache(maxsize=4096)
+def _bwd_workspace_size(h: int, N: int) -> int:
+    return B.fldce_logprob_bwd_workspace_size(h, N)
+
+
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
-    return None if t is None else t.data_ptr()
+    # (an empty tensor may have no address)
+    return None if t is None or t.numel() == 0 else t.data_ptr()
 
 
 def _forward(x, weight, bias, token, h, top_k):
@@ -115,14 +121,12 @@ class FusedLinearLogProbsFunction(torch.autograd.Function):
             dH = torch.empty_like(x) if need_x else None
             dW = torch.empty_like(weight) if need_w else None
             db = torch.empty_like(bias) if need_b else None
-            nbytes = B.fldce_logprob_bwd_workspace_size(ctx.h, N)
+            nbytes = _bwd_workspace_size(ctx.h, N)
             ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-            call = B.make_logprob_grad_call(
-                H=x, W=weight, bias=bias, token=token, N=N, lse=lse, entropy=entropy,
-                dlogprob=dlogprob, dentropy=dentropy, dH=dH, dW=dW, db=db,
-                workspace=ws, workspace_bytes=nbytes,
-                stream=torch.cuda.current_stream(dev))
-            B.fldce_logprob_bwd(ctx.h, call)
+            B.fldce_logprob_bwd(ctx.h, B.fldce_logprob_grad_call(
+                _ptr(x), weight.data_ptr(), _ptr(bias), _ptr(token), N, _ptr(lse), _ptr(entropy),
+                _ptr(dlogprob), _ptr(dentropy), _ptr(dH), _ptr(dW), _ptr(db), ws.data_ptr(),
+                nbytes, None, raw_stream(dev)))
         return dH, dW, db, None, None, None
 
 

@@ -142,5 +142,5 @@ def linear_w4(x: torch.Tensor, weight: W4Weight, bias: Optional[torch.Tensor] = 
     with on_device_of(x2):
         out = torch.empty((x2.shape[0], V), dtype=out_dtype, device=x.device)
         B.fldce_w4_linear(x2, x2.shape[0], weight.packed, weight.scales, weight.group_size, bias,
-                          V, D, out, code, raw_stream(x.device))
+                          V, D, out, code, stream=raw_stream(x.device))
     return out if x.dim() == 2 else out.view(*x.shape[:-1], V)

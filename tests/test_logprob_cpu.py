@@ -181,12 +181,12 @@ def test_w4_call_refusals():
     assert _status(q, A, 0, 0, 64, 32, A, A, 0) == B.FLDCE_ERR_INVALID_ARG
     assert _status(q, A, 0, 10, 64, 32, A + 4, A, 0) == B.FLDCE_ERR_ALIGN
     f = B.fldce_w4_linear
-    assert _status(f, A, -1, A, A, 32, None, 10, 64, A, 0, 0) == B.FLDCE_ERR_INVALID_ARG
-    assert _status(f, A, 1, A, A, 48, None, 10, 64, A, 0, 0) == B.FLDCE_ERR_UNSUPPORTED
-    assert _status(f, A, 1, A, A, 32, None, 10, 64, A, 5, 0) == B.FLDCE_ERR_UNSUPPORTED
-    assert _status(f, None, 1, A, A, 32, None, 10, 64, A, 0, 0) == B.FLDCE_ERR_INVALID_ARG
-    assert _status(f, A + 2, 1, A, A, 32, None, 10, 64, A, 0, 0) == B.FLDCE_ERR_ALIGN
-    assert _status(f, A, 1, A, A, 32, None, 10, 64, A + 2, 1, 0) == B.FLDCE_ERR_ALIGN
+    assert _status(f, A, -1, A, A, 32, None, 10, 64, A, 0, None, 0) == B.FLDCE_ERR_INVALID_ARG
+    assert _status(f, A, 1, A, A, 48, None, 10, 64, A, 0, None, 0) == B.FLDCE_ERR_UNSUPPORTED
+    assert _status(f, A, 1, A, A, 32, None, 10, 64, A, 5, None, 0) == B.FLDCE_ERR_UNSUPPORTED
+    assert _status(f, None, 1, A, A, 32, None, 10, 64, A, 0, None, 0) == B.FLDCE_ERR_INVALID_ARG
+    assert _status(f, A + 2, 1, A, A, 32, None, 10, 64, A, 0, None, 0) == B.FLDCE_ERR_ALIGN
+    assert _status(f, A, 1, A, A, 32, None, 10, 64, A + 2, 1, None, 0) == B.FLDCE_ERR_ALIGN
 
 
 def test_workspace_grows_with_tokens_and_alternatives():

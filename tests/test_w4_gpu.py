@@ -120,7 +120,9 @@ def test_rows_past_the_call_stay():
     x, _, w, _ = make(12, 64, 301, 32)
     from linear_diffusion_cross_b200 import binding as B
     out = torch.full((12, 301), 7.0, device=DEV)
-    B.fldce_w4_linear(x, 5, w.packed, w.scales, 32, None, 301, 64, out, B.FLDCE_FP32)
+    err = torch.full((2,), 7, dtype=torch.int32, device=DEV)
+    B.fldce_w4_linear(x, 5, w.packed, w.scales, 32, None, 301, 64, out, B.FLDCE_FP32, err)
+    assert err.tolist() == [0, 0]
     assert (out[5:] == 7.0).all() and torch.equal(out[:5], linear_w4(x[:5], w))
 
 
