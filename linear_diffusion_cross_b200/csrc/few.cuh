@@ -225,6 +225,8 @@ k_few(const __grid_constant__ FewParams p) {
         tma_prefetch_desc(&p.xmap);
     }
     __syncthreads();
+    // the merge may be made ready to start (it waits for this grid to end)
+    if (KC >= 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t r_begin = (int64_t)blockIdx.x * p.cta_rows;
     const int64_t r_end = min(p.V, r_begin + p.cta_rows);
 
@@ -476,6 +478,7 @@ k_few(const __grid_constant__ FewParams p) {
         // barrier): i = 32 (slice + wpt j) + lane
         const int64_t v0 = r_begin + (int64_t)t * kFewRows;
         const int rows = (int)max((int64_t)0, min((int64_t)tile_rows, r_end - v0));
+        const int js = 8 / min(wpt, 8);                     // 32-row runs of a warp
         float bias[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -540,6 +543,7 @@ k_few(const __grid_constant__ FewParams p) {
                 const float ref = rs[q].rebase(mx, p.c);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
+                    if (j >= js) break;
                     rs[q].add(a[j], ref, p.c);
                     if constexpr (KC > 0)
                         wt[q].offer(a[j], (int)(v0 + 32 * (slice + wpt * j) + lane), lane);

@@ -442,6 +442,9 @@ __global__ void __launch_bounds__(THREADS) k_logprob_merge(const LpMergeParams p
     __shared__ float sm_mag[4][KA + 1];
     const float4* stats = p.parts.stats + row;
     const size_t ld = p.parts.ld;
+    // launched while the kernel before may still run: wait for its results
+    // (returns at once after an ordinary launch)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // ---- statistics: a thread's first slices stay in registers between passes
     float4 kept[kMergeKeep];

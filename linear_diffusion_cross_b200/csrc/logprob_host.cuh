@@ -271,9 +271,19 @@ int lp_forward(fldce_plan* h, const fldce_logprob_call& call, const LpLayout& L,
         // a few rows: the latency of one is the kernel's
         if (!bf16)
             k_logprob_merge<KC, float, 128><<<rows, 128, 0, st>>>(mp);
-        else if (rows <= kFewTokens)
-            k_logprob_merge<KC, __nv_bfloat16, 512><<<rows, 512, 0, st>>>(mp);
-        else
+        else if (rows <= kFewTokens) {
+            // behind k_few: launched early, its set-up hidden in that kernel's end
+            cudaLaunchAttribute early{};
+            early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            early.val.programmaticStreamSerializationAllowed = 1;
+            cudaLaunchConfig_t lc{};
+            lc.gridDim = dim3((unsigned)rows);
+            lc.blockDim = dim3(512);
+            lc.stream = st;
+            lc.attrs = &early;
+            lc.numAttrs = 1;
+            FLDCE_CUDA(cudaLaunchKernelEx(&lc, k_logprob_merge<KC, __nv_bfloat16, 512>, mp));
+        } else
             k_logprob_merge<KC, __nv_bfloat16, 128><<<rows, 128, 0, st>>>(mp);
         FLDCE_CUDA(cudaGetLastError());
         prof_mark(h, PK_MERGE, st);
