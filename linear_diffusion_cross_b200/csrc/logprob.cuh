@@ -358,6 +358,13 @@ __device__ __forceinline__ void dot_share(const T* __restrict__ x, const HeadWei
     }
 }
 
+// dst[0, n) = src[0, n_src) and zeros after it, in 16-byte vectors.
+__global__ void k_pad_rows(const uint4* __restrict__ src, int64_t n_src, uint4* __restrict__ dst,
+                           int64_t n) {
+    const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+    if (i < n) dst[i] = i < n_src ? src[i] : make_uint4(0, 0, 0, 0);
+}
+
 struct LpMergeParams {
     LpParts parts;
     int n_parts;

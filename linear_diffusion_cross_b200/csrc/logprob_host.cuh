@@ -15,8 +15,29 @@ namespace {
 constexpr size_t kLpBudget = size_t(1) << 30;
 constexpr int64_t kW4ChunkTokens = 256;         // tokens of a forward chunk on a 4-bit weight
 
+// TMA loads from a tensor map that spans less than 128 KiB in all run at a
+// fraction of their speed (measured, whatever the box, pitch or alignment: a
+// sweep over 32000 x 1024 takes 58 us for 63 tokens and 24 us for 64), so
+// fewer hidden states than that are copied and padded with zero rows.
+constexpr size_t kSmallMap = size_t(128) << 10;
+bool pads_rows(int64_t rows, int64_t D) { return (size_t)rows * D * 2 < kSmallMap; }
+int64_t padded_rows(int64_t D) { return cdiv((int64_t)kSmallMap, 2 * D); }
+
+// H [rows, D] bf16 as the maps should see it: itself, or its padded copy in buf.
+cudaError_t pad_rows(const void** H, int64_t* map_rows, void* buf, int64_t rows, int64_t D,
+                     cudaStream_t st) {
+    *map_rows = rows;
+    if (!pads_rows(rows, D)) return cudaSuccess;
+    *map_rows = padded_rows(D);
+    const int64_t n = *map_rows * (D / 8);
+    k_pad_rows<<<(unsigned)cdiv(n, 256), 256, 0, st>>>(static_cast<const uint4*>(*H),
+                                                       rows * (D / 8), static_cast<uint4*>(buf), n);
+    *H = buf;
+    return cudaGetLastError();
+}
+
 struct LpLayout {
-    size_t cnt, stats, top, floor, total;
+    size_t cnt, stats, top, floor, hpad, total;
     int64_t C;                // tokens per chunk
     int64_t n_parts;
     int kc;
@@ -42,6 +63,7 @@ LpLayout lp_layout(const fldce_plan* p, int64_t N, int top_k, bool w4) {
     L.stats = take((size_t)L.n_parts * L.C * 16);
     L.top = take((size_t)L.n_parts * L.C * L.kc * 8);
     L.floor = take((size_t)L.C * 4 * (L.kc + 1));
+    L.hpad = take((size_t)padded_rows(p->cfg.D) * p->cfg.D * 2);
     L.total = off;
     return L;
 }
@@ -52,7 +74,7 @@ LpLayout lp_layout(const fldce_plan* p, int64_t N, int top_k, bool w4) {
 constexpr int kLpFewRowsSplits = 16;
 int lp_max_splits(int64_t C) { return C <= 256 ? kLpFewRowsSplits : kMaxKSplits; }
 
-Layout lp_bwd_layout(const fldce_plan* p, int64_t N) {
+Layout lp_bwd_layout(const fldce_plan* p, int64_t N, size_t* hpad = nullptr) {
     Layout L{};
     const int64_t C = std::max<int64_t>(1, std::min<int64_t>(p->chunk, N));
     L.C = C;
@@ -76,6 +98,8 @@ Layout lp_bwd_layout(const fldce_plan* p, int64_t N) {
     L.dw_acc = take(acc ? (size_t)p->cfg.V * p->cfg.D * 4 : 0);
     L.db_part = take((size_t)kColsumSegs * p->cfg.V * 4);
     L.db_acc = take((size_t)p->cfg.V * 4);
+    const size_t h = take(bf16 ? (size_t)padded_rows(p->cfg.D) * p->cfg.D * 2 : 0);
+    if (hpad != nullptr) *hpad = h;
     L.total = off;
     return L;
 }
@@ -235,7 +259,10 @@ int lp_forward(fldce_plan* h, const fldce_logprob_call& call, const LpLayout& L,
             }
         } else if (bf16) {
             CUtensorMap mH;
-            if (!make_map(&mH, Hc, D, rows, D, 64, 128)) return FLDCE_ERR_CUDA;
+            const void* Hm = Hc;
+            int64_t map_rows;
+            FLDCE_CUDA(pad_rows(&Hm, &map_rows, ws + L.hpad, rows, D, st));
+            if (!make_map(&mH, Hm, D, map_rows, D, 64, 128)) return FLDCE_ERR_CUDA;
             const SweepParams<KC> sp{
                 c, neg, V, rows, static_cast<const __nv_bfloat16*>(call.bias), parts};
             FLDCE_CUDA(launch_sweep<KC>(mH, mW, rows, V, D, sp, &cnt->dev_err, dev.sms, st));
@@ -383,7 +410,8 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
     if (!aligned_to(c.token, 8) || !aligned_to(c.lse, 4) || !aligned_to(c.entropy, 4) ||
         !aligned_to(c.dlogprob, 4) || !aligned_to(c.dentropy, 4) || !aligned_to(c.err_count, 4))
         return FLDCE_ERR_ALIGN;
-    const Layout L = lp_bwd_layout(h, N);
+    size_t hpad = 0;
+    const Layout L = lp_bwd_layout(h, N, &hpad);
     if (c.workspace_bytes < L.total) return FLDCE_ERR_WORKSPACE;
     DeviceInfo dev;
     if (int s = check_device(&dev)) return s;
@@ -429,10 +457,13 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
         if (bf16) {
             CUtensorMap mH_k, mH_mn, mG_k, mG_mn;
             LogprobGEpi::Params gp;
+            const void* Hm = Hc;
+            int64_t map_rows;
+            FLDCE_CUDA(pad_rows(&Hm, &map_rows, ws + hpad, rows, D, st));
             // (whole boxes of rows: rows past the tokens get zeros)
             if (!make_store_map(&gp.gmap, G, V, round_up((size_t)rows, 32), h->Vpad, 2) ||
-                !make_map(&mH_k, Hc, D, rows, D, 64, 128) ||
-                !make_map(&mH_mn, Hc, D, rows, D, 64, 64) ||
+                !make_map(&mH_k, Hm, D, map_rows, D, 64, 128) ||
+                !make_map(&mH_mn, Hm, D, map_rows, D, 64, 64) ||
                 !make_map(&mG_k, G, V, rows, h->Vpad, 64, 128) ||
                 !make_map(&mG_mn, G, V, rows, h->Vpad, 64, 64))
                 return FLDCE_ERR_CUDA;
