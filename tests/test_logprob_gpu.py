@@ -230,6 +230,9 @@ def check_grads(x, y, w, b, s, a, e, **kw):
     (1, 8, 1, 1.0, False, 0),
     (1, 64, 300, 1.0, True, 0),
     (5, 72, 257, -0.8, True, 0),
+    (16, 264, 777, 1.0, True, 0),
+    (31, 96, 1501, -1.0, False, 0),
+    (40, 96, 33001, 0.5, True, 32),
     (100, 136, 1003, 0.5, False, 0),
     (300, 256, 2000, 1.0, True, 128),
     (257, 520, 3001, 1.0, False, 100),
@@ -541,6 +544,33 @@ def test_beside_the_loss():
     lim = R.grad_bounds(x, w, A, dH, dW, db, R.bound_z(x, w, b, 1.0), BF, 200)
     for p, q, tol in zip(g1, g2, lim):
         assert bool(((p.double() - q.double()).abs() <= 2 * tol).all())
+
+
+def test_calls_cut_into_chunks():
+    # more tokens than the partial statistics of one chunk hold (1024 here)
+    N, D, V = 1100, 8, 600000
+    x, y, w, b = make(N, D, V, BF, bias=True)
+    whole = fused_linear_logprobs(x, y, w, b, top_k=20)
+    t = 2 * R.bounds(x, w, b, 1.0)["entropy"]
+    for a, e in ((0, 5), (1000, 1100), (1030, 1031)):
+        r = fused_linear_logprobs(x[a:e], y[a:e], w, b, top_k=20)
+        assert torch.equal(r.top_ids, whole.top_ids[a:e])
+        for p, q in zip(r, whole):
+            if p.is_floating_point():
+                close(p, q[a:e], t, "chunk")
+    z, lp, ent, lse, ids, top = R.forward(x[1020:1040], y[1020:1040], w, b, k=20)
+    assert torch.equal(whole.top_ids[1020:1040], ids)
+    close(whole.lse[1020:1040], lse, t, "lse")
+
+
+def test_every_token_count():
+    # where kernels change with the number of tokens: 8, 16, 24, 32 and 256,
+    # and below and above 128 KiB of hidden states
+    x, y, w, b = make(300, 512, 1501, BF, bias=True)
+    a, e = torch.randn(300, device=DEV), torch.randn(300, device=DEV)
+    for n in (1, 7, 8, 9, 15, 16, 17, 23, 24, 25, 31, 32, 33, 63, 127, 128, 129, 255, 256, 257):
+        check_forward(x[:n], y[:n], w, b, k=3)
+        check_grads(x[:n], y[:n], w, b, 1.0, a[:n], e[:n])
 
 
 def test_long_vocabulary_offsets():

@@ -85,6 +85,16 @@ def test_logprobs(N, D, V, group):
         check_forward(x, y, w, b, s, k, wref=whole(w))
 
 
+def test_many_tokens():
+    # several passes over the weight, several chunks of rows
+    x, y, w, b = make(530, 96, 1111, 32, bias=True)
+    check_forward(x, y, w, b, k=4, wref=whole(w))
+    wr = whole(w)
+    ref = x.double() @ wr.T + b.double()
+    err = (linear_w4(x, w, b).double() - ref).abs()
+    assert bool((err <= R.bound_z(x, wr, b, 1.0) + 2.0 ** -24 * ref.abs()).all())
+
+
 def test_extreme_nibbles_and_scales():
     # every weight -8 (which quantize_w4 never writes), huge and tiny scales side by side
     V, D = 300, 128
