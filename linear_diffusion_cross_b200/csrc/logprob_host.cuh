@@ -69,10 +69,14 @@ LpLayout lp_layout(const fldce_plan* p, int64_t N, int top_k, bool w4) {
 }
 
 // Workspace of the gradient.  G has room for whole 32-row store boxes; dH of
-// few tokens, whose products have few tiles, may be split over K more often
-// than the loss's (16 partials of up to 256 rows are small).
-constexpr int kLpFewRowsSplits = 16;
-int lp_max_splits(int64_t C) { return C <= 256 ? kLpFewRowsSplits : kMaxKSplits; }
+// few tokens or columns, whose product has few tiles, may be split over K
+// more often than the loss's, up to 16 ways while the partials stay small.
+constexpr int kLpSplits = 16;
+constexpr int64_t kLpSplitBytes = int64_t(64) << 20;
+int lp_max_splits(int64_t C, int64_t D) {
+    const int64_t part = (int64_t)round_up((size_t)C, 256) * D * 4;
+    return (int)std::max<int64_t>(kMaxKSplits, std::min<int64_t>(kLpSplits, kLpSplitBytes / part));
+}
 
 Layout lp_bwd_layout(const fldce_plan* p, int64_t N, size_t* hpad = nullptr) {
     Layout L{};
@@ -93,7 +97,7 @@ Layout lp_bwd_layout(const fldce_plan* p, int64_t N, size_t* hpad = nullptr) {
     L.row_y = take(C * 4);
     L.loss_tok = take(C * 4);
     L.G = take(round_up((size_t)C, 32) * p->Vpad * p->elt);
-    L.dh_acc = take(bf16 ? (size_t)lp_max_splits(C) * round_up((size_t)C, 256) * p->cfg.D * 4 : 0);
+    L.dh_acc = take(bf16 ? (size_t)lp_max_splits(C, p->cfg.D) * round_up((size_t)C, 256) * p->cfg.D * 4 : 0);
     const bool acc = (L.nchunks > 1 || (dw_accumulate(p) && N > 0)) && !dw_out_fp32(p);
     L.dw_acc = take(acc ? (size_t)p->cfg.V * p->cfg.D * 4 : 0);
     L.db_part = take((size_t)kColsumSegs * p->cfg.V * 4);
@@ -493,7 +497,7 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
             }
             prof_mark(h, PK_G, st);
             const GradGemm gg{h,  &L,   ws, cnt,       &dev,
-                              st, rows, r0, DynRows(), lp_max_splits(L.C)};
+                              st, rows, r0, DynRows(), lp_max_splits(L.C, D)};
             if (c.dH != nullptr)
                 if (int e = gg.dh(mG_k, mW_mn, c.dH)) return e;
             if (c.dW != nullptr)
