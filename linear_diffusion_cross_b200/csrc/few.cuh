@@ -517,8 +517,12 @@ k_few(const __grid_constant__ FewParams p) {
                     const int i = 32 * (slice + wpt * j) + lane;
                     if (i >= rows) continue;
                     float gr = lp_grad(fmaf(a[j], p.c2, -L2), kap, ee);
-                    if (v0 + i == y) gr += ta;
-                    o[i] = __float2bfloat16_rn(dead ? 0.f : gr);
+                    if (dead) gr = 0.f;
+                    else if (v0 + i == y) {
+                        gr += ta;
+                        p.k.res[tok] = bf16_rest(gr);
+                    }
+                    o[i] = __float2bfloat16_rn(gr);
                 }
             } else if constexpr (KC < 0) {
                 const int64_t o = (int64_t)tok * p.V + v0;

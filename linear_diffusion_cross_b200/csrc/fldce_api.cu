@@ -297,14 +297,14 @@ cudaError_t launch_fused_gdh(const CUtensorMap& mH, const CUtensorMap& mW, const
     return cudaGetLastError();
 }
 
-// db (+)= column sums of the chunk's G, in a fixed order (two passes).
-cudaError_t launch_colsum(const void* G, bool g_bf16, int64_t ldg, int rows, int64_t V,
-                          float* part, float* acc, bool add, cudaStream_t st,
-                          const int32_t* dyn_count = nullptr, int dyn_base = 0,
-                          int seg_min = 256) {
-    const int nseg = (int)std::min<int64_t>(kColsumSegs, std::max<int64_t>(1, cdiv(rows, seg_min)));
-    const int seg_rows = (int)cdiv(rows, nseg);
-    const dim3 grid((unsigned)cdiv(cdiv(V, 2), 128), (unsigned)nseg);
+// Column sums of the chunk's G in *nseg row segments (at least seg_min rows
+// each): part[segment][V].
+cudaError_t launch_colsum_partial(const void* G, bool g_bf16, int64_t ldg, int rows, int64_t V,
+                                  float* part, cudaStream_t st, int seg_min, int* nseg,
+                                  const int32_t* dyn_count = nullptr, int dyn_base = 0) {
+    *nseg = (int)std::min<int64_t>(kColsumSegs, std::max<int64_t>(1, cdiv(rows, seg_min)));
+    const int seg_rows = (int)cdiv(rows, *nseg);
+    const dim3 grid((unsigned)cdiv(cdiv(V, 2), 128), (unsigned)*nseg);
     if (g_bf16)
         k_colsum_partial<__nv_bfloat16><<<grid, 128, 0, st>>>(
             static_cast<const __nv_bfloat16*>(G), ldg, rows, V, seg_rows, part, dyn_count,
@@ -312,6 +312,17 @@ cudaError_t launch_colsum(const void* G, bool g_bf16, int64_t ldg, int rows, int
     else
         k_colsum_partial<float><<<grid, 128, 0, st>>>(static_cast<const float*>(G), ldg, rows, V,
                                                       seg_rows, part, dyn_count, dyn_base);
+    return cudaGetLastError();
+}
+
+// db (+)= column sums of the chunk's G, in a fixed order (two passes).
+cudaError_t launch_colsum(const void* G, bool g_bf16, int64_t ldg, int rows, int64_t V,
+                          float* part, float* acc, bool add, cudaStream_t st,
+                          const int32_t* dyn_count = nullptr, int dyn_base = 0) {
+    int nseg = 0;
+    cudaError_t e = launch_colsum_partial(G, g_bf16, ldg, rows, V, part, st, 256, &nseg, dyn_count,
+                                          dyn_base);
+    if (e != cudaSuccess) return e;
     k_colsum_final<<<(unsigned)cdiv(V, 256), 256, 0, st>>>(part, nseg, V, acc, add ? 1 : 0);
     return cudaGetLastError();
 }

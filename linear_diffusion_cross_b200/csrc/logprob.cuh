@@ -694,13 +694,20 @@ struct LpCoef {
     float* ee;
     float* ta;
     int32_t* y;          // validated token or -1
+    // What rounding to bf16 took off G at the token's column (set by the
+    // sweep): that element is most of a row, and db gets it back.
+    float* res;
 };
 
 __global__ void k_logprob_coef(const int64_t* __restrict__ token, const float* __restrict__ lse,
                                const float* __restrict__ entropy, const float* __restrict__ dlp,
                                const float* __restrict__ dent, int rows, int64_t V,
-                               int64_t ignore_index, float s, LpCoef o, int32_t* n_err) {
-    const int i = blockIdx.x * blockDim.x + threadIdx.x;
+                               int64_t ignore_index, float s, LpCoef o, int32_t* n_err,
+                               const uint4* __restrict__ src, int64_t n_src,
+                               uint4* __restrict__ dst, int64_t n_dst) {
+    const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+    // the padded copy of the hidden states, where they need one (see k_pad_rows)
+    if (i < n_dst) dst[i] = i < n_src ? src[i] : make_uint4(0, 0, 0, 0);
     if (i >= rows) return;
     int64_t y = token != nullptr ? token[i] : ignore_index;
     if (y != ignore_index && (y < 0 || y >= V)) {
@@ -717,6 +724,76 @@ __global__ void k_logprob_coef(const int64_t* __restrict__ token, const float* _
     o.ee[i] = s * e * 0.69314718055994530942f;
     o.ta[i] = s * a;
     o.y[i] = has ? (int32_t)y : -1;
+    o.res[i] = 0.f;
+}
+
+// Column sums of the bf16 G [rows, Vpad] over one segment of rows (in row
+// order): part[segment][V], four columns a thread, 16 rows' loads in flight.
+__global__ void __launch_bounds__(128)
+k_logprob_colsum(const __nv_bfloat16* __restrict__ G, int64_t ldg, int rows, int64_t V,
+                 int seg_rows, float* __restrict__ part) {
+    const int64_t v = 4 * ((int64_t)blockIdx.x * blockDim.x + threadIdx.x);
+    if (v >= V) return;
+    const int r0 = blockIdx.y * seg_rows;
+    const int r1 = min(rows, r0 + seg_rows);
+    float a[4] = {};
+#pragma unroll 16
+    for (int r = r0; r < r1; ++r) {
+        const uint2 w = __ldcs(reinterpret_cast<const uint2*>(G + (size_t)r * ldg + v));
+        a[0] += __uint_as_float(w.x << 16);
+        a[1] += __uint_as_float(w.x & 0xffff0000u);
+        a[2] += __uint_as_float(w.y << 16);
+        a[3] += __uint_as_float(w.y & 0xffff0000u);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (v + i < V) part[(size_t)blockIdx.y * V + v + i] = a[i];
+}
+
+// db of one chunk: the column sums' partials (in segment order), what rounding
+// took off G at the chunk's tokens (in token order), and the chunks before.
+// The last chunk writes db (out), added to with `add_out`; others acc.
+__global__ void k_logprob_db(const float* __restrict__ part, int nseg, int64_t V,
+                             const int32_t* __restrict__ y, const float* __restrict__ res, int rows,
+                             float* __restrict__ acc, int add_acc, void* out, int to_bf16,
+                             int add_out) {
+    __shared__ __align__(16) int32_t sy[256];
+    __shared__ float sr[256];
+    const int64_t v = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    float s = 0.f;
+    if (v < V)
+        for (int k = 0; k < nseg; ++k) s += part[(size_t)k * V + v];
+    for (int r0 = 0; r0 < rows; r0 += 256) {
+        __syncthreads();
+        const int r = r0 + threadIdx.x;
+        sy[threadIdx.x] = r < rows ? y[r] : -1;
+        sr[threadIdx.x] = r < rows ? res[r] : 0.f;
+        __syncthreads();
+        const int n = min(256, rows - r0);
+#pragma unroll 4
+        for (int i = 0; i < n; i += 4) {
+            const int4 q = *reinterpret_cast<const int4*>(sy + i);
+            if (q.x == v || q.y == v || q.z == v || q.w == v)         // seldom
+                for (int j = 0; j < 4; ++j)
+                    if (sy[i + j] == v) s += sr[i + j];
+        }
+    }
+    if (v >= V) return;
+    if (add_acc) s += acc[v];
+    if (out == nullptr) {
+        acc[v] = s;
+    } else if (to_bf16) {
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out);
+        o[v] = __float2bfloat16_rn(add_out ? __bfloat162float(o[v]) + s : s);
+    } else {
+        float* o = static_cast<float*>(out);
+        o[v] = add_out ? o[v] + s : s;
+    }
+}
+
+// What rounding x to bf16 takes off it.
+__device__ __forceinline__ float bf16_rest(float x) {
+    return x - __bfloat162float(__float2bfloat16_rn(x));
 }
 
 // One element: q = log2 p.  A row without upstream gradient is exactly 0.
@@ -775,7 +852,10 @@ struct LogprobGEpi {
             if ((unsigned)(yrel - 32 * j) < 32u) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                    if (i == yrel - 32 * j) g[i] += ta;
+                    if (i == yrel - 32 * j) {
+                        g[i] += ta;
+                        p.k.res[m] = dead ? 0.f : bf16_rest(g[i]);
+                    }
             }
             if (dead) {
 #pragma unroll

@@ -71,6 +71,7 @@ LpLayout lp_layout(const fldce_plan* p, int64_t N, int top_k, bool w4) {
 // Workspace of the gradient.  G has room for whole 32-row store boxes; dH of
 // few tokens or columns, whose product has few tiles, may be split over K
 // more often than the loss's, up to 16 ways while the partials stay small.
+constexpr int kLpColsumSegs = 16;               // row segments of db's column sums
 constexpr int kLpSplits = 16;
 constexpr int64_t kLpSplitBytes = int64_t(64) << 20;
 int lp_max_splits(int64_t C, int64_t D) {
@@ -96,11 +97,12 @@ Layout lp_bwd_layout(const fldce_plan* p, int64_t N, size_t* hpad = nullptr) {
     L.row_gcoef = take(C * 4);
     L.row_y = take(C * 4);
     L.loss_tok = take(C * 4);
+    L.part_sz = take(C * 4);
     L.G = take(round_up((size_t)C, 32) * p->Vpad * p->elt);
     L.dh_acc = take(bf16 ? (size_t)lp_max_splits(C, p->cfg.D) * round_up((size_t)C, 256) * p->cfg.D * 4 : 0);
     const bool acc = (L.nchunks > 1 || (dw_accumulate(p) && N > 0)) && !dw_out_fp32(p);
     L.dw_acc = take(acc ? (size_t)p->cfg.V * p->cfg.D * 4 : 0);
-    L.db_part = take((size_t)kColsumSegs * p->cfg.V * 4);
+    L.db_part = take((size_t)kLpColsumSegs * p->cfg.V * 4);
     L.db_acc = take((size_t)p->cfg.V * 4);
     const size_t h = take(bf16 ? (size_t)padded_rows(p->cfg.D) * p->cfg.D * 2 : 0);
     if (hpad != nullptr) *hpad = h;
@@ -438,7 +440,7 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
     }
     LpCoef k{reinterpret_cast<float*>(ws + L.row_lse2), reinterpret_cast<float*>(ws + L.row_gcoef),
              reinterpret_cast<float*>(ws + L.zy), reinterpret_cast<float*>(ws + L.loss_tok),
-             reinterpret_cast<int32_t*>(ws + L.row_y)};
+             reinterpret_cast<int32_t*>(ws + L.row_y), reinterpret_cast<float*>(ws + L.part_sz)};
     float* db_part = reinterpret_cast<float*>(ws + L.db_part);
     float* db_acc = reinterpret_cast<float*>(ws + L.db_acc);
     CUtensorMap mW_k, mW_mn;
@@ -448,22 +450,25 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
     for (int64_t ci = 0; ci < L.nchunks; ++ci) {
         const int64_t r0 = ci * h->chunk;
         const int rows = (int)std::min<int64_t>(h->chunk, N - r0);
-        k_logprob_coef<<<(unsigned)cdiv(rows, 256), 256, 0, st>>>(
+        const uint8_t* Hc = static_cast<const uint8_t*>(c.H) + (size_t)r0 * D * h->elt;
+        const bool pads = bf16 && pads_rows(rows, D);
+        const int64_t map_rows = pads ? padded_rows(D) : rows;
+        const int64_t n_pad = pads ? map_rows * (D / 8) : 0;
+        uint4* hp = reinterpret_cast<uint4*>(ws + hpad);
+        k_logprob_coef<<<(unsigned)cdiv(std::max<int64_t>(rows, n_pad), 256), 256, 0, st>>>(
             c.token != nullptr ? c.token + r0 : nullptr, c.lse + r0,
             c.entropy != nullptr ? c.entropy + r0 : nullptr,
             c.dlogprob != nullptr ? c.dlogprob + r0 : nullptr,
             c.dentropy != nullptr ? c.dentropy + r0 : nullptr, rows, V, cfg.ignore_index,
-            cfg.logit_scale, k, c.err_count);
+            cfg.logit_scale, k, c.err_count, reinterpret_cast<const uint4*>(Hc), rows * (D / 8), hp,
+            n_pad);
         FLDCE_CUDA(cudaGetLastError());
         prof_mark(h, PK_MERGE, st);
-        const uint8_t* Hc = static_cast<const uint8_t*>(c.H) + (size_t)r0 * D * h->elt;
         void* G = ws + L.G;
         if (bf16) {
             CUtensorMap mH_k, mH_mn, mG_k, mG_mn;
             LogprobGEpi::Params gp;
-            const void* Hm = Hc;
-            int64_t map_rows;
-            FLDCE_CUDA(pad_rows(&Hm, &map_rows, ws + hpad, rows, D, st));
+            const void* Hm = pads ? static_cast<const void*>(hp) : Hc;
             // (whole boxes of rows: rows past the tokens get zeros)
             if (!make_store_map(&gp.gmap, G, V, round_up((size_t)rows, 32), h->Vpad, 2) ||
                 !make_map(&mH_k, Hm, D, map_rows, D, 64, 128) ||
@@ -523,13 +528,22 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
             }
         }
         if (c.db != nullptr) {
-            FLDCE_CUDA(launch_colsum(G, bf16, h->Vpad, rows, V, db_part, db_acc, ci > 0, st,
-                                     nullptr, 0, 32));
-            if (ci + 1 == L.nchunks) {
-                k_cast_out<<<(unsigned)cdiv(V, 256), 256, 0, st>>>(
-                    db_acc, c.db, V, dw_out_fp32(h) ? 0 : 1, accum ? 1 : 0);
+            int nseg = (int)std::min<int64_t>(kLpColsumSegs, cdiv(rows, 32));
+            if (bf16) {
+                const dim3 grid((unsigned)cdiv(V, 512), (unsigned)nseg);
+                k_logprob_colsum<<<grid, 128, 0, st>>>(static_cast<const __nv_bfloat16*>(G),
+                                                       h->Vpad, rows, V, (int)cdiv(rows, nseg),
+                                                       db_part);
                 FLDCE_CUDA(cudaGetLastError());
+            } else {
+                FLDCE_CUDA(launch_colsum_partial(G, false, h->Vpad, rows, V, db_part, st, 32,
+                                                 &nseg));
             }
+            const bool last = ci + 1 == L.nchunks;
+            k_logprob_db<<<(unsigned)cdiv(V, 256), 256, 0, st>>>(
+                db_part, nseg, V, k.y, k.res, bf16 ? rows : 0, db_acc, ci > 0 ? 1 : 0,
+                last ? c.db : nullptr, dw_out_fp32(h) ? 0 : 1, accum ? 1 : 0);
+            FLDCE_CUDA(cudaGetLastError());
             prof_mark(h, PK_DB, st);
         }
     }
