@@ -194,9 +194,9 @@ __device__ __forceinline__ void consumers_sync() {
 }
 
 // KC >= 0: statistics and KC candidates per (CTA, token).  -1: logits.
-// -2: the logits' gradient (as LogprobGEpi, for few tokens: that kernel's
-// 256-row tiles of H, nearly empty, make every SM read the same few lines of
-// L2 at a time: 957 us for 6 tokens of 3920 x 159722, 215 us here).
+// -2: the logits' gradient (as LogprobGEpi, whose 256-row tiles are nearly
+// empty here: G of 32 tokens of 3920 x 159722 takes that kernel 294 us, this
+// one 215 us for 6, the weight's bytes alone 191).
 // LB: log2 of a 4-bit weight's group in 32-element blocks.
 template <bool W4, int LB, int NT, int KC>
 __global__ void __launch_bounds__(FewCfg<W4, LB, NT>::THREADS, 1)
@@ -521,6 +521,7 @@ k_few(const __grid_constant__ FewParams p) {
                     else if (v0 + i == y) {
                         gr += ta;
                         p.k.res[tok] = bf16_rest(gr);
+                        if (p.k.first != nullptr) atomicMin(p.k.first + y, tok);
                     }
                     o[i] = __float2bfloat16_rn(gr);
                 }

@@ -145,7 +145,8 @@ bool make_store_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t ro
 }
 
 // The store map of `p` and the plain view of the same matrix.
-bool set_store(StoreEpi::Params* p, int mode, void* base, int64_t cols, int64_t rows, int elt) {
+template <class P>
+bool set_store(P* p, int mode, void* base, int64_t cols, int64_t rows, int elt) {
     p->mode = mode;
     p->out = base;
     p->rows = rows;
@@ -329,15 +330,24 @@ cudaError_t launch_colsum(const void* G, bool g_bf16, int64_t ldg, int rows, int
 
 // dst = sum of k fp32 partials `stride` floats apart (bf16 or fp32 out).
 cudaError_t launch_sum_splits(const float* part, int64_t stride, int k, void* dst, bool to_bf16,
-                              int64_t n, int sms, cudaStream_t st) {
+                              int64_t n, int sms, cudaStream_t st, const RowRest& rest = RowRest{},
+                              int64_t D = 8) {
     const int64_t n8 = n / 8;
     if (n8 == 0) return cudaSuccess;
     const int blocks = (int)std::min<int64_t>(cdiv(n8, 256), 8 * (int64_t)sms);
-    if (to_bf16)
-        k_sum_splits<__nv_bfloat16><<<blocks, 256, 0, st>>>(
-            part, stride, k, static_cast<__nv_bfloat16*>(dst), n8);
-    else
-        k_sum_splits<float><<<blocks, 256, 0, st>>>(part, stride, k, static_cast<float*>(dst), n8);
+    const int d8 = (int)(D / 8);
+    auto* ob = static_cast<__nv_bfloat16*>(dst);
+    auto* of = static_cast<float*>(dst);
+    if (rest.first != nullptr) {
+        if (to_bf16)
+            k_sum_splits<__nv_bfloat16, true><<<blocks, 256, 0, st>>>(part, stride, k, ob, n8, rest, d8);
+        else
+            k_sum_splits<float, true><<<blocks, 256, 0, st>>>(part, stride, k, of, n8, rest, d8);
+    } else if (to_bf16) {
+        k_sum_splits<__nv_bfloat16, false><<<blocks, 256, 0, st>>>(part, stride, k, ob, n8, rest, d8);
+    } else {
+        k_sum_splits<float, false><<<blocks, 256, 0, st>>>(part, stride, k, of, n8, rest, d8);
+    }
     return cudaGetLastError();
 }
 
@@ -507,16 +517,29 @@ struct GradGemm {
     int64_t r0;               // first token of the chunk
     DynRows dyn;              // compacted rows (dim is set per product)
     int max_splits = kMaxKSplits;   // K splits of dH that L->dh_acc has room for
+    // What rounding took off G, given back (first null: nothing is).
+    RowRest dh_rest{};
+    RowRest dw_rest{};
 
     // dH = G W (K = V).  When one pass over the tiles leaves many SMs
     // idle in its last round, the vocabulary is split into k ranges;
     // split j stores its fp32 partial in its own buffer and one pass
     // sums them in split order (deterministic) into dH.
     int dh(const CUtensorMap& mG_k, const CUtensorMap& mW_mn, void* dH) const {
+        const DhPlan dp = plan_dh(rows, h->cfg.D, h->cfg.V, std::max(1, dev->sms / 2), max_splits);
+        // (with K splits, the pass that sums them gives back the rest)
+        return dp.k_splits == 1 && dh_rest.first != nullptr ? dh_as<true>(dp, mG_k, mW_mn, dH)
+                                                            : dh_as<false>(dp, mG_k, mW_mn, dH);
+    }
+
+    template <bool REST>
+    int dh_as(const DhPlan& dp, const CUtensorMap& mG_k, const CUtensorMap& mW_mn, void* dH) const {
+        using Epi = StoreEpiT<REST>;
         const int64_t D = h->cfg.D, V = h->cfg.V;
-        const DhPlan dp = plan_dh(rows, D, V, std::max(1, dev->sms / 2), max_splits);
         const int ks = dp.k_splits;
-        StoreEpi::Params hp;
+        typename Epi::Params hp;
+        hp.rest = dh_rest;
+        hp.rest_rows = rows;
         const bool dh_fp32 = (h->cfg.flags & FLDCE_FLAG_DH_FP32) != 0;
         float* part = reinterpret_cast<float*>(ws + L->dh_acc);
         const int split_rows = (int)round_up((size_t)rows, 256);
@@ -533,15 +556,15 @@ struct GradGemm {
         const Walk dh_walk{1, ks, kOneBlock};
         const DynRows dr{dyn.count, dyn.base, 1};
         if (dp.wide)
-            FLDCE_CUDA((launch_gemm<CfgKM2, StoreEpi>(mG_k, mW_mn, rows, D, V, dh_walk, hp,
+            FLDCE_CUDA((launch_gemm<CfgKM2, Epi>(mG_k, mW_mn, rows, D, V, dh_walk, hp,
                                                       &cnt->dev_err, dev->sms, st, dr)));
         else
-            FLDCE_CUDA((launch_gemm<CfgKM, StoreEpi>(mG_k, mW_mn, rows, D, V, dh_walk, hp,
+            FLDCE_CUDA((launch_gemm<CfgKM, Epi>(mG_k, mW_mn, rows, D, V, dh_walk, hp,
                                                      &cnt->dev_err, dev->sms, st, dr)));
         prof_mark(h, PK_DH, st);
         if (ks > 1) {
             FLDCE_CUDA(launch_sum_splits(part, (int64_t)split_rows * D, ks, dHc, !dh_fp32,
-                                         (int64_t)rows * D, dev->sms, st));
+                                         (int64_t)rows * D, dev->sms, st, dh_rest, D));
             prof_mark(h, PK_CONVERT, st);
         }
         return FLDCE_OK;
@@ -550,10 +573,19 @@ struct GradGemm {
     // dW = G^T H (K = tokens of the chunk): one chunk writes dW directly;
     // several store, then reduce-add, fp32 partial sums.
     int dw(const CUtensorMap& mG_mn, const CUtensorMap& mH_mn, void* dW, int64_t ci) const {
+        return dw_rest.first != nullptr ? dw_as<true>(mG_mn, mH_mn, dW, ci)
+                                        : dw_as<false>(mG_mn, mH_mn, dW, ci);
+    }
+
+    template <bool REST>
+    int dw_as(const CUtensorMap& mG_mn, const CUtensorMap& mH_mn, void* dW, int64_t ci) const {
+        using Epi = StoreEpiT<REST>;
         const int64_t D = h->cfg.D, V = h->cfg.V;
         const bool fp32_dw = dw_out_fp32(h), accum = dw_accumulate(h);
         float* dw_ws = fp32_dw ? static_cast<float*>(dW) : reinterpret_cast<float*>(ws + L->dw_acc);
-        StoreEpi::Params wp;
+        typename Epi::Params wp;
+        wp.rest = dw_rest;
+        wp.rest_rows = (int)V;
         if (L->nchunks == 1 && !fp32_dw && !accum) {
             if (!set_store(&wp, OUT_BF16, dW, D, V, 2)) return FLDCE_ERR_CUDA;
         } else {
@@ -563,7 +595,7 @@ struct GradGemm {
             if (!set_store(&wp, mode, dw_ws, D, V, 4)) return FLDCE_ERR_CUDA;
         }
         const Walk dw_walk{1, 1, kOneBlock};
-        FLDCE_CUDA((launch_gemm<CfgMM, StoreEpi>(mG_mn, mH_mn, (int)V, D, rows, dw_walk, wp,
+        FLDCE_CUDA((launch_gemm<CfgMM, Epi>(mG_mn, mH_mn, (int)V, D, rows, dw_walk, wp,
                                                  &cnt->dev_err, dev->sms, st,
                                                  DynRows{dyn.count, dyn.base, 2})));
         prof_mark(h, PK_DW, st);

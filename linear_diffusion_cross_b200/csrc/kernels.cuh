@@ -353,13 +353,41 @@ struct GEpi {
 // that a later pass sums in a fixed order.
 //
 // A 32-row box that hangs over the last row is written by its lanes instead
-// (one row each): a TMA store takes 0.7 us for every row outside the map
-// (measured: G of 6 rows, 957 us against 294 us for 32 rows), which is the
-// tail of the whole product when the vocabulary is no multiple of 32.
+// (one row each), and no store box reaches outside its map.
+//
+// With REST (the gradient of the log-probabilities) a row gets back, before it
+// is rounded, what rounding took off single elements of G (see RowRest).
 // ======================================================================
 enum StoreMode { OUT_BF16 = 0, WS_STORE = 1, WS_ADD = 2 };
 
-struct StoreEpi {
+// Row r of the product G X has one large element G[r, first[r]] (next null:
+// dH, X = W), or column r of G has one at every token that r is the target of
+// (dW, X = H): n = first[r], next[n], ... in increasing order.  out[r] gets
+// rest X back for them: rest[r], or rest[n], is what rounding to bf16 took
+// off the element.  The first four tokens of a target are enough: with n more
+// of them, the rounding errors that stay add up to sqrt(n) of one, against a
+// sum of 4 + n: at most a quarter of what one does to one token's row.
+struct RowRest {
+    const int32_t* first = nullptr;  // [rows]; outside [0, end) where there is none
+    const int32_t* next = nullptr;   // [tokens]; >= end after the last
+    const float* rest = nullptr;     // [tokens]
+    const __nv_bfloat16* X = nullptr;
+    int end = 0;
+};
+constexpr int kRowRests = 4;
+
+// Eight bf16 values of a 16-byte vector.
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        f[2 * k] = __uint_as_float(u[k] << 16);
+        f[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+    }
+}
+
+template <bool REST>
+struct StoreEpiT {
     struct Params {
         CUtensorMap omap;        // bf16 [rows, cols] box 64 x 32, or fp32 box 32 x 32
         int mode;
@@ -367,7 +395,79 @@ struct StoreEpi {
         void* out = nullptr;     // the map's matrix: rows x cols, rows `cols` apart
         int64_t rows = 0;
         int64_t cols = 0;
+        RowRest rest;
+        int rest_rows = 0;       // rows that have one
     };
+
+    static constexpr bool kAhead = REST;
+    struct Rest {
+        int src[kRowRests];      // rows of X and what this lane's row gets of them
+        float e[kRowRests];
+        uint4 x[4];              // the next 32 columns of the first one
+        bool any;                // of the warp's rows
+    };
+
+    static __device__ __forceinline__ int peek(const Params& p, const TileCtx& t) {
+        const int row = t.row0 + t.split * p.split_rows + 32 * t.q + t.lane;
+        return row < p.rest_rows ? p.rest.first[row] : -1;
+    }
+
+    template <class Cfg>
+    static __device__ __forceinline__ Rest ahead(const Params& p, const TileCtx& t, int n) {
+        Rest a{};
+        a.any = __any_sync(0xffffffffu, n >= 0 && n < p.rest.end);
+        if (!a.any) return a;
+        const int row = t.row0 + t.split * p.split_rows + 32 * t.q + t.lane;
+        const bool chains = p.rest.next != nullptr;
+#pragma unroll
+        for (int l = 0; l < kRowRests; ++l) {
+            if (n < 0 || n >= p.rest.end) break;
+            a.src[l] = n;
+            a.e[l] = p.rest.rest[chains ? n : row];
+            if (l == 0) fetch(p, a, t.col0);
+            n = chains ? p.rest.next[n] : -1;
+        }
+        return a;
+    }
+
+    // Columns [c0, c0 + 32) of the first row of X (D is a multiple of 8).
+    static __device__ __forceinline__ void fetch(const Params& p, Rest& a, int64_t c0) {
+        const __nv_bfloat16* x = p.rest.X + (int64_t)a.src[0] * p.cols + c0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (c0 + 8 * q < p.cols) a.x[q] = __ldg(reinterpret_cast<const uint4*>(x) + q);
+    }
+
+    static __device__ __forceinline__ void add8(uint32_t* r, float e, const uint4& x) {
+        float w[8];
+        unpack8(x, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            r[i] = __float_as_uint(fmaf(e, w[i], __uint_as_float(r[i])));
+    }
+
+    // r += rest X[., c0 ..] for the rows of X that this lane's row has.  The
+    // first one's columns were fetched a chunk before (else each chunk waits
+    // for the L2: dW of 1001 tokens of 32000 x 2048 124 us, 96 us without).
+    static __device__ __forceinline__ void give_back(const Params& p, Rest& a, int64_t c0,
+                                                     bool last, uint32_t (&r)[32]) {
+        if (!a.any) return;
+        if (a.e[0] != 0.f) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (c0 + 8 * q < p.cols) add8(r + 8 * q, a.e[0], a.x[q]);
+            if (!last) fetch(p, a, c0 + 32);
+        }
+#pragma unroll
+        for (int l = 1; l < kRowRests; ++l) {
+            if (a.e[l] == 0.f) continue;
+            const __nv_bfloat16* x = p.rest.X + (int64_t)a.src[l] * p.cols + c0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (c0 + 8 * q < p.cols)
+                    add8(r + 8 * q, a.e[l], __ldg(reinterpret_cast<const uint4*>(x) + q));
+        }
+    }
 
     // Columns [c0, c0 + 32) of row `row` from this lane's accumulator row.
     static __device__ __forceinline__ void put_row(const Params& p, int64_t row, int64_t c0,
@@ -399,11 +499,22 @@ struct StoreEpi {
     template <class Cfg>
     static __device__ __forceinline__ void run(const Params& p, const TileCtx& t,
                                                const AccRow& acc, Stager& st) {
+        Rest none;
+        run<Cfg>(p, t, acc, st, none);
+    }
+
+    template <class Cfg>
+    static __device__ __forceinline__ void run(const Params& p, const TileCtx& t,
+                                               const AccRow& acc, Stager& st, Rest& rest) {
         const int64_t n0 = t.col0;
         const int y = t.row0 + t.split * p.split_rows + 32 * t.q;
         const int mode = p.mode;
         const bool hangs_over = y + 32 > p.rows;       // the same for the whole warp
-        for_each_chunk<Cfg::NCHUNK>(acc, [&](const uint32_t (&r)[32], int j) {
+        for_each_chunk<Cfg::NCHUNK>(acc, [&](const uint32_t (&rin)[32], int j) {
+            uint32_t r[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = rin[i];
+            if constexpr (REST) give_back(p, rest, n0 + 32 * j, j + 1 == Cfg::NCHUNK, r);
             if (hangs_over) {
                 put_row(p, y + t.lane, n0 + 32 * j, r);
             } else if (mode == OUT_BF16) {
@@ -423,6 +534,8 @@ struct StoreEpi {
         });
     }
 };
+
+using StoreEpi = StoreEpiT<false>;
 
 // ======================================================================
 // Row kernels shared by both element types.
@@ -927,9 +1040,11 @@ __global__ void k_f32_to_bf16(const float* __restrict__ src, __nv_bfloat16* __re
 // out[i] = sum_j part[j * stride + i], j = 0 .. k-1 in that order (the K
 // splits of one GEMM), so the result does not depend on which split
 // finished first.  n8 = elements / 8.
-template <class OutT>
+// REST: each row gets rest X back for its one large element (see RowRest);
+// d8 = columns / 8.
+template <class OutT, bool REST>
 __global__ void k_sum_splits(const float* __restrict__ part, int64_t stride, int k,
-                             OutT* __restrict__ out, int64_t n8) {
+                             OutT* __restrict__ out, int64_t n8, RowRest rest, int d8) {
     for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n8;
          i += (int64_t)gridDim.x * blockDim.x) {
         float4 a = reinterpret_cast<const float4*>(part)[2 * i];
@@ -939,6 +1054,20 @@ __global__ void k_sum_splits(const float* __restrict__ part, int64_t stride, int
             const float4 c = q[2 * i], d = q[2 * i + 1];
             a.x += c.x; a.y += c.y; a.z += c.z; a.w += c.w;
             b.x += d.x; b.y += d.y; b.z += d.z; b.w += d.w;
+        }
+        if constexpr (REST) {
+            const int64_t row = i / d8;
+            const int n = rest.first[row];
+            const float e = n >= 0 && n < rest.end ? rest.rest[row] : 0.f;
+            if (e != 0.f) {
+                float w[8];
+                unpack8(__ldg(reinterpret_cast<const uint4*>(rest.X) + (int64_t)n * d8 +
+                              (i - row * d8)), w);
+                a.x = fmaf(e, w[0], a.x); a.y = fmaf(e, w[1], a.y);
+                a.z = fmaf(e, w[2], a.z); a.w = fmaf(e, w[3], a.w);
+                b.x = fmaf(e, w[4], b.x); b.y = fmaf(e, w[5], b.y);
+                b.z = fmaf(e, w[6], b.z); b.w = fmaf(e, w[7], b.w);
+            }
         }
         if constexpr (sizeof(OutT) == 2) {
             uint4 w;

@@ -271,15 +271,6 @@ __device__ __forceinline__ int nibble(uint32_t w, int i) {
     return ((int)(w << (28 - 4 * i))) >> 28;       // two's complement
 }
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        f[2 * k] = __uint_as_float(u[k] << 16);
-        f[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
-    }
-}
-
 constexpr int kDots = 4;             // rows of W per group of dot products
 
 // This thread's share of <x, W_v[j]> (z) and of sum |x_i w_i| (mag), j <
@@ -695,8 +686,12 @@ struct LpCoef {
     float* ta;
     int32_t* y;          // validated token or -1
     // What rounding to bf16 took off G at the token's column (set by the
-    // sweep): that element is most of a row, and db gets it back.
+    // sweep): that element is most of a row, and its rounding would be as
+    // large an error as the rounding of the results.  dH, dW and db get it
+    // back; for dW a column's tokens are chained in increasing order.
     float* res;
+    int32_t* first;      // [V] first token whose target this is (set by the sweep), or huge
+    int32_t* next;       // [chunk] next token with this token's target, or rows
 };
 
 __global__ void k_logprob_coef(const int64_t* __restrict__ token, const float* __restrict__ lse,
@@ -706,8 +701,31 @@ __global__ void k_logprob_coef(const int64_t* __restrict__ token, const float* _
                                const uint4* __restrict__ src, int64_t n_src,
                                uint4* __restrict__ dst, int64_t n_dst) {
     const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
-    // the padded copy of the hidden states, where they need one (see k_pad_rows)
+    // the padded copy of the hidden states, where they need one (see pads_rows)
     if (i < n_dst) dst[i] = i < n_src ? src[i] : make_uint4(0, 0, 0, 0);
+    if (o.first != nullptr) {
+        if (i < V) o.first[i] = 0x7fffffff;
+        // a warp for every token looks for the next one of the same target
+        const int64_t n = i >> 5;
+        if (n < rows && token != nullptr) {
+            const int64_t t = token[n];
+            const int lane = (int)(i & 31);
+            int64_t found = rows;
+            for (int64_t b = n + 1; b < rows; b += 128) {
+                unsigned hit[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int64_t j = b + 32 * q + lane;
+                    hit[q] = __ballot_sync(0xffffffffu, j < rows && token[j] == t);
+                }
+#pragma unroll
+                for (int q = 3; q >= 0; --q)
+                    if (hit[q] != 0) found = b + 32 * q + __ffs(hit[q]) - 1;
+                if (found < rows) break;
+            }
+            if (lane == 0) o.next[n] = (int32_t)found;
+        }
+    }
     if (i >= rows) return;
     int64_t y = token != nullptr ? token[i] : ignore_index;
     if (y != ignore_index && (y < 0 || y >= V)) {
@@ -791,9 +809,10 @@ __global__ void k_logprob_db(const float* __restrict__ part, int nseg, int64_t V
     }
 }
 
-// What rounding x to bf16 takes off it.
+// What rounding x to bf16 takes off it (nothing where either is no number).
 __device__ __forceinline__ float bf16_rest(float x) {
-    return x - __bfloat162float(__float2bfloat16_rn(x));
+    const float r = x - __bfloat162float(__float2bfloat16_rn(x));
+    return fabsf(r) < CUDART_INF_F ? r : 0.f;
 }
 
 // One element: q = log2 p.  A row without upstream gradient is exactly 0.
@@ -855,6 +874,7 @@ struct LogprobGEpi {
                     if (i == yrel - 32 * j) {
                         g[i] += ta;
                         p.k.res[m] = dead ? 0.f : bf16_rest(g[i]);
+                        if (p.k.first != nullptr) atomicMin(p.k.first + n0 + yrel, m);
                     }
             }
             if (dead) {

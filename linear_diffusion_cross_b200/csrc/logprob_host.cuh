@@ -98,6 +98,8 @@ Layout lp_bwd_layout(const fldce_plan* p, int64_t N, size_t* hpad = nullptr) {
     L.row_y = take(C * 4);
     L.loss_tok = take(C * 4);
     L.part_sz = take(C * 4);
+    L.part_am = take(bf16 ? C * 4 : 0);
+    L.part_ml = take(bf16 ? (size_t)p->cfg.V * 4 : 0);
     L.G = take(round_up((size_t)C, 32) * p->Vpad * p->elt);
     L.dh_acc = take(bf16 ? (size_t)lp_max_splits(C, p->cfg.D) * round_up((size_t)C, 256) * p->cfg.D * 4 : 0);
     const bool acc = (L.nchunks > 1 || (dw_accumulate(p) && N > 0)) && !dw_out_fp32(p);
@@ -440,7 +442,9 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
     }
     LpCoef k{reinterpret_cast<float*>(ws + L.row_lse2), reinterpret_cast<float*>(ws + L.row_gcoef),
              reinterpret_cast<float*>(ws + L.zy), reinterpret_cast<float*>(ws + L.loss_tok),
-             reinterpret_cast<int32_t*>(ws + L.row_y), reinterpret_cast<float*>(ws + L.part_sz)};
+             reinterpret_cast<int32_t*>(ws + L.row_y), reinterpret_cast<float*>(ws + L.part_sz),
+             nullptr, reinterpret_cast<int32_t*>(ws + L.part_am)};
+    if (bf16 && c.dW != nullptr) k.first = reinterpret_cast<int32_t*>(ws + L.part_ml);
     float* db_part = reinterpret_cast<float*>(ws + L.db_part);
     float* db_acc = reinterpret_cast<float*>(ws + L.db_acc);
     CUtensorMap mW_k, mW_mn;
@@ -455,7 +459,9 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
         const int64_t map_rows = pads ? padded_rows(D) : rows;
         const int64_t n_pad = pads ? map_rows * (D / 8) : 0;
         uint4* hp = reinterpret_cast<uint4*>(ws + hpad);
-        k_logprob_coef<<<(unsigned)cdiv(std::max<int64_t>(rows, n_pad), 256), 256, 0, st>>>(
+        const int64_t n_thr = std::max({k.first != nullptr ? std::max<int64_t>(V, 32 * (int64_t)rows)
+                                                           : (int64_t)rows, n_pad});
+        k_logprob_coef<<<(unsigned)cdiv(n_thr, 256), 256, 0, st>>>(
             c.token != nullptr ? c.token + r0 : nullptr, c.lse + r0,
             c.entropy != nullptr ? c.entropy + r0 : nullptr,
             c.dlogprob != nullptr ? c.dlogprob + r0 : nullptr,
@@ -501,8 +507,11 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
                                                             &cnt->dev_err, dev.sms, st)));
             }
             prof_mark(h, PK_G, st);
-            const GradGemm gg{h,  &L,   ws, cnt,       &dev,
-                              st, rows, r0, DynRows(), lp_max_splits(L.C, D)};
+            GradGemm gg{h,  &L,   ws, cnt,       &dev,
+                        st, rows, r0, DynRows(), lp_max_splits(L.C, D)};
+            gg.dh_rest = RowRest{k.y, nullptr, k.res, static_cast<const __nv_bfloat16*>(c.W), (int)V};
+            gg.dw_rest = RowRest{k.first, k.next, k.res, reinterpret_cast<const __nv_bfloat16*>(Hc),
+                                 rows};
             if (c.dH != nullptr)
                 if (int e = gg.dh(mG_k, mW_mn, c.dH)) return e;
             if (c.dW != nullptr)

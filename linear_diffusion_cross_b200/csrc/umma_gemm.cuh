@@ -163,6 +163,14 @@ struct TileCtx {
     int lane;
 };
 
+// What an epilogue fetches before a tile's accumulator is there, where it has
+// such: Epi::peek(params, tile) loads one word a lane while the tile before is
+// written, and Epi::ahead<Cfg>(params, tile, word) what follows from it.
+template <class Epi, class = void>
+struct has_ahead : std::false_type {};
+template <class Epi>
+struct has_ahead<Epi, std::enable_if_t<Epi::kAhead>> : std::true_type {};
+
 // Per-thread view of one accumulator row handed to an epilogue functor.
 struct AccRow {
     uint32_t taddr;       // TMEM address of this thread's lane, column 0 of the tile
@@ -399,21 +407,39 @@ umma_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         Stager st{smem_u32(epi_smem) + (uint32_t)(q * 2) * Cfg::EPI_BUF_BYTES, lane, 0};
         const uint32_t lead_tempty0 = mapa_shared(tempty_bar(0), 0);
         uint32_t lt = 0;
-        for (int u = pair; u < units && !*abort_flag; u += npairs, ++lt) {
+        auto tile_of = [&](int u) {
             int mt, nt, split, k0, k1;
             unit_coords(u, mt, nt, split, k0, k1);
+            return TileCtx{rows_dyn, mt * Cfg::PAIR_M + (int)rank * Cfg::BM, (int64_t)nt * Cfg::BN,
+                           split, row, q, lane};
+        };
+        TileCtx next{};
+        [[maybe_unused]] int word = 0;
+        if (pair < units) {
+            next = tile_of(pair);
+            if constexpr (has_ahead<Epi>::value) word = Epi::peek(ep, next);
+        }
+        for (int u = pair; u < units && !*abort_flag; u += npairs, ++lt) {
+            const TileCtx t = next;
             const int b = Cfg::NBUF == 2 ? (int)(lt & 1u) : 0;
             const uint32_t use = Cfg::NBUF == 2 ? lt >> 1 : lt;
+            auto more = [&] {
+                if constexpr (has_ahead<Epi>::value) return Epi::template ahead<Cfg>(ep, t, word);
+                else return 0;
+            }();
+            if (u + npairs < units) {
+                next = tile_of(u + npairs);
+                if constexpr (has_ahead<Epi>::value) word = Epi::peek(ep, next);
+            }
             if (!mbar_wait_bounded(tfull_bar(b), use & 1u, kWaitLimitNs)) {
                 fail();
                 break;
             }
             tc_fence_after();
-            TileCtx t{rows_dyn, mt * Cfg::PAIR_M + (int)rank * Cfg::BM, (int64_t)nt * Cfg::BN,
-                      split, row, q, lane};
             AccRow acc{tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * Cfg::BN),
                        lead_tempty0 + 8u * (uint32_t)b, lane};
-            Epi::template run<Cfg>(ep, t, acc, st);
+            if constexpr (has_ahead<Epi>::value) Epi::template run<Cfg>(ep, t, acc, st, more);
+            else Epi::template run<Cfg>(ep, t, acc, st);
         }
         st.drain();
     }

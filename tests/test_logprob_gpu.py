@@ -307,6 +307,35 @@ def test_gradients_against_differences():
             assert abs(d - float(g.view(-1)[j])) <= 2e-5 * max(1.0, abs(d))
 
 
+@pytest.mark.parametrize("N,V,chunk", [(9, 5000, 0), (150, 1500, 0), (150, 9000, 0),
+                                       (700, 1999, 0), (300, 5000, 128)])
+def test_targets_rounding_is_given_back(N, V, chunk):
+    """The target's element of a 16-bit G, nine tenths of the way to the middle
+    between two 16-bit numbers, must not cost dH and dW its rounding.  W is zero
+    but for the targets, so that the rest of G hardly matters."""
+    D = 72
+    x, _, w, _ = make(N, D, V, BF, seed=N)
+    ids = torch.randperm(V, device=DEV)
+    y = ids[torch.arange(N, device=DEV) % (N // 2 + 1)]          # once or twice each
+    y = y[torch.randperm(N, device=DEV)]
+    keep = torch.zeros(V, 1, device=DEV, dtype=BF)
+    keep[y] = 1
+    w = w * keep * 2.0 ** -6                                     # nearly flat: p = 1 / V
+    a = torch.full((N,), (1 + 0.9 * 2.0 ** -8) / (1 - 1 / V), device=DEV)
+    got, _ = grads_of(x, y, w, None, 1.0, a, None, chunk_n=chunk)
+    dH, dW, db, A = R.grads(x, y, w, None, 1.0, a, None)
+    B_ = A.clone()
+    B_[torch.arange(N, device=DEV), y] = 0                       # what stays rounded
+    u, dz = 2.0 ** -8, R.bound_z(x, w, None, 1.0)
+    xa, wa = x.double().abs(), w.double().abs()
+    # fp32: p's relative error, every accumulation, the rest's own rounding
+    fp = 4 * dz + 2.0 ** -18
+    for t, want, big, small, n in ((got[0], dH, A @ wa, B_ @ wa, V), (got[1], dW, A.T @ xa, B_.T @ xa, N)):
+        lim = u * want.abs() + u * (1 + u) * small + (fp + n * 2.0 ** -23) * big * (1 + u)
+        err = (t.double() - want).abs()
+        assert bool((err <= lim + 1e-30).all()), float((err / (lim + 1e-30)).max())
+
+
 def test_only_the_gradients_asked_for():
     x, y, w, b = make(40, 64, 700, BF, bias=True)
     full, _ = grads_of(x, y, w, b, 1.0, torch.ones(40, device=DEV), None)
