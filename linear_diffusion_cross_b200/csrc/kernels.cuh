@@ -364,17 +364,21 @@ enum StoreMode { OUT_BF16 = 0, WS_STORE = 1, WS_ADD = 2 };
 // dH, X = W), or column r of G has one at every token that r is the target of
 // (dW, X = H): n = first[r], next[n], ... in increasing order.  out[r] gets
 // rest X back for them: rest[r], or rest[n], is what rounding to bf16 took
-// off the element.  The first four tokens of a target are enough: with n more
-// of them, the rounding errors that stay add up to sqrt(n) of one, against a
-// sum of 4 + n: at most a quarter of what one does to one token's row.
+// off the element.  The epilogue does it for a target's first token; the sum
+// over those from the second on is in a row of `more` (r's, or the second
+// token's: whichever there are fewer of), made by a kernel before
+// (k_logprob_repeats).  All of them count: dW's sum over n tokens of
+// either sign grows as sqrt(n), and so do the roundings (with four of 256
+// given back, the rows of dW are 1.46 times as far off as once-rounded ones).
 struct RowRest {
     const int32_t* first = nullptr;  // [rows]; outside [0, end) where there is none
     const int32_t* next = nullptr;   // [tokens]; >= end after the last
     const float* rest = nullptr;     // [tokens]
     const __nv_bfloat16* X = nullptr;
     int end = 0;
+    const float* more = nullptr;     // [rows or tokens][columns]
+    bool more_by_row = false;
 };
-constexpr int kRowRests = 4;
 
 // Eight bf16 values of a 16-byte vector.
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
@@ -401,9 +405,10 @@ struct StoreEpiT {
 
     static constexpr bool kAhead = REST;
     struct Rest {
-        int src[kRowRests];      // rows of X and what this lane's row gets of them
-        float e[kRowRests];
-        uint4 x[4];              // the next 32 columns of the first one
+        int src;                 // row of X, and how much of it this lane's row gets
+        float e;
+        uint4 x[4];              // its next 32 columns
+        const float* more;       // the sum over the other tokens, or null
         bool any;                // of the warp's rows
     };
 
@@ -418,21 +423,20 @@ struct StoreEpiT {
         a.any = __any_sync(0xffffffffu, n >= 0 && n < p.rest.end);
         if (!a.any) return a;
         const int row = t.row0 + t.split * p.split_rows + 32 * t.q + t.lane;
-        const bool chains = p.rest.next != nullptr;
-#pragma unroll
-        for (int l = 0; l < kRowRests; ++l) {
-            if (n < 0 || n >= p.rest.end) break;
-            a.src[l] = n;
-            a.e[l] = p.rest.rest[chains ? n : row];
-            if (l == 0) fetch(p, a, t.col0);
-            n = chains ? p.rest.next[n] : -1;
+        if (n < 0 || n >= p.rest.end) return a;
+        a.src = n;
+        a.e = p.rest.rest[p.rest.next != nullptr ? n : row];
+        fetch(p, a, t.col0);
+        if (p.rest.next != nullptr) {
+            const int m = p.rest.next[n];
+            if (m < p.rest.end) a.more = p.rest.more + (int64_t)(p.rest.more_by_row ? row : m) * p.cols;
         }
         return a;
     }
 
-    // Columns [c0, c0 + 32) of the first row of X (D is a multiple of 8).
+    // Columns [c0, c0 + 32) of the row of X (D is a multiple of 8).
     static __device__ __forceinline__ void fetch(const Params& p, Rest& a, int64_t c0) {
-        const __nv_bfloat16* x = p.rest.X + (int64_t)a.src[0] * p.cols + c0;
+        const __nv_bfloat16* x = p.rest.X + (int64_t)a.src * p.cols + c0;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
             if (c0 + 8 * q < p.cols) a.x[q] = __ldg(reinterpret_cast<const uint4*>(x) + q);
@@ -446,26 +450,28 @@ struct StoreEpiT {
             r[i] = __float_as_uint(fmaf(e, w[i], __uint_as_float(r[i])));
     }
 
-    // r += rest X[., c0 ..] for the rows of X that this lane's row has.  The
-    // first one's columns were fetched a chunk before (else each chunk waits
-    // for the L2: dW of 1001 tokens of 32000 x 2048 124 us, 96 us without).
+    // r += rest X[., c0 ..] for what this lane's row has.  The columns of X
+    // were fetched a chunk before (else each chunk waits for the L2: dW of 1001
+    // tokens of 32000 x 2048 124 us, 96 us without).
     static __device__ __forceinline__ void give_back(const Params& p, Rest& a, int64_t c0,
                                                      bool last, uint32_t (&r)[32]) {
         if (!a.any) return;
-        if (a.e[0] != 0.f) {
+        if (a.e != 0.f) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                if (c0 + 8 * q < p.cols) add8(r + 8 * q, a.e[0], a.x[q]);
+                if (c0 + 8 * q < p.cols) add8(r + 8 * q, a.e, a.x[q]);
             if (!last) fetch(p, a, c0 + 32);
         }
+        if (a.more != nullptr) {
 #pragma unroll
-        for (int l = 1; l < kRowRests; ++l) {
-            if (a.e[l] == 0.f) continue;
-            const __nv_bfloat16* x = p.rest.X + (int64_t)a.src[l] * p.cols + c0;
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (c0 + 8 * q < p.cols)
-                    add8(r + 8 * q, a.e[l], __ldg(reinterpret_cast<const uint4*>(x) + q));
+            for (int q = 0; q < 8; ++q) {
+                if (c0 + 4 * q >= p.cols) break;
+                const float4 m = __ldg(reinterpret_cast<const float4*>(a.more + c0) + q);
+                r[4 * q] = __float_as_uint(__uint_as_float(r[4 * q]) + m.x);
+                r[4 * q + 1] = __float_as_uint(__uint_as_float(r[4 * q + 1]) + m.y);
+                r[4 * q + 2] = __float_as_uint(__uint_as_float(r[4 * q + 2]) + m.z);
+                r[4 * q + 3] = __float_as_uint(__uint_as_float(r[4 * q + 3]) + m.w);
+            }
         }
     }
 

@@ -745,6 +745,109 @@ __global__ void k_logprob_coef(const int64_t* __restrict__ token, const float* _
     o.res[i] = 0.f;
 }
 
+// What the tokens of a target from the second on give back to its row of dW:
+// the sum of res[n] H[n] in fp32 and in the tokens' order, in row y (by_row)
+// or the second token's row of `sum`, eight columns a thread.  A block looks
+// for the first tokens of targets among every gridDim.x-th token (they are
+// frequent at the chunk's begin).
+//
+// A link to the next token costs a load's latency, so where it is near, the
+// block looks through the next 1024 tokens at once instead, and adds the rows
+// it finds with 16 loads in flight (1001 tokens that share one target of
+// 32000 x 2048, backward to dW: 579 us with links alone, 430 to 500 with
+// windows).
+constexpr int kRepeatWindow = 1024;
+constexpr int kRepeatNear = 256;
+__global__ void __launch_bounds__(128)
+k_logprob_repeats(LpCoef k, int rows, const __nv_bfloat16* __restrict__ H, int64_t D, bool by_row,
+                  float* __restrict__ sum) {
+    __shared__ int list[kRepeatWindow];
+    __shared__ uint32_t found[kRepeatWindow / 32];
+    __shared__ int second[128], heads;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int64_t d = 8 * ((int64_t)blockIdx.y * blockDim.x + tid);
+    for (int64_t b = blockIdx.x; b < rows; b += 128 * (int64_t)gridDim.x) {
+        if (tid == 0) heads = 0;
+        __syncthreads();
+        const int64_t c = b + tid * (int64_t)gridDim.x;
+        if (c < rows) {
+            const int yc = k.y[c], nc = k.next[c];
+            if (yc >= 0 && nc < rows && k.first[yc] == c) second[atomicAdd(&heads, 1)] = nc;
+        }
+        __syncthreads();
+        const int count = heads;
+        for (int s = 0; s < count; ++s) {
+            float a[8] = {};
+            int n = second[s];
+            const int y = k.y[n];
+            float* const out = sum + (int64_t)(by_row ? y : n) * D + d;
+            while (n < rows) {
+                const int next = k.next[n];
+                int size = 1;
+                __syncthreads();                       // the list is free again
+                if (next - n >= kRepeatNear || next >= rows) {
+                    if (tid == 0) list[0] = n;
+                    __syncthreads();
+                    n = next;
+                } else {
+                    // tokens n + 128 i + tid: bit `lane` of word 4 i + warp
+#pragma unroll
+                    for (int i = 0; i < kRepeatWindow / 128; ++i) {
+                        const int64_t t = (int64_t)n + 128 * i + tid;
+                        const uint32_t bits = __ballot_sync(0xffffffffu, t < rows && k.y[t] == y);
+                        if (lane == 0) found[4 * i + (tid >> 5)] = bits;
+                    }
+                    __syncthreads();
+                    // lane i of every warp: words 0 .. i
+                    const uint32_t word = found[lane];
+                    int upto = __popc(word);
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+                        if (lane >= o) upto += v;
+                    }
+                    size = __shfl_sync(0xffffffffu, upto, 31);
+#pragma unroll
+                    for (int i = 0; i < kRepeatWindow / 128; ++i) {
+                        const int w = 4 * i + (tid >> 5);
+                        const uint32_t bits = __shfl_sync(0xffffffffu, word, w);
+                        const int before = __shfl_sync(0xffffffffu, upto, w) - __popc(bits);
+                        if (bits >> lane & 1u)
+                            list[before + __popc(bits & ((1u << lane) - 1u))] = n + 32 * w + lane;
+                    }
+                    __syncthreads();
+                    n = k.next[list[size - 1]];
+                }
+                if (d >= D) continue;
+                for (int j = 0; j < size; j += 16) {
+                    float e[16];
+                    uint4 x[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const bool is = j + i < size;
+                        const int64_t t = is ? list[j + i] : 0;
+                        e[i] = is ? __ldg(k.res + t) : 0.f;
+                        x[i] = is ? __ldg(reinterpret_cast<const uint4*>(H + t * D + d))
+                                  : make_uint4(0, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        if (e[i] == 0.f) continue;
+                        float f[8];
+                        unpack8(x[i], f);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) a[q] = fmaf(e[i], f[q], a[q]);
+                    }
+                }
+            }
+            if (d >= D) continue;
+            reinterpret_cast<float4*>(out)[0] = make_float4(a[0], a[1], a[2], a[3]);
+            reinterpret_cast<float4*>(out)[1] = make_float4(a[4], a[5], a[6], a[7]);
+        }
+        __syncthreads();
+    }
+}
+
 // Column sums of the bf16 G [rows, Vpad] over one segment of rows (in row
 // order): part[segment][V], four columns a thread, 16 rows' loads in flight.
 __global__ void __launch_bounds__(128)

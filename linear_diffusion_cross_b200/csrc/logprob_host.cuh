@@ -79,8 +79,12 @@ int lp_max_splits(int64_t C, int64_t D) {
     return (int)std::max<int64_t>(kMaxKSplits, std::min<int64_t>(kLpSplits, kLpSplitBytes / part));
 }
 
-Layout lp_bwd_layout(const fldce_plan* p, int64_t N, size_t* hpad = nullptr) {
-    Layout L{};
+struct LpBwdLayout : Layout {
+    size_t hpad, repeats;
+};
+
+LpBwdLayout lp_bwd_layout(const fldce_plan* p, int64_t N) {
+    LpBwdLayout L{};
     const int64_t C = std::max<int64_t>(1, std::min<int64_t>(p->chunk, N));
     L.C = C;
     L.nchunks = N > 0 ? cdiv(N, p->chunk) : 0;
@@ -106,8 +110,8 @@ Layout lp_bwd_layout(const fldce_plan* p, int64_t N, size_t* hpad = nullptr) {
     L.dw_acc = take(acc ? (size_t)p->cfg.V * p->cfg.D * 4 : 0);
     L.db_part = take((size_t)kLpColsumSegs * p->cfg.V * 4);
     L.db_acc = take((size_t)p->cfg.V * 4);
-    const size_t h = take(bf16 ? (size_t)padded_rows(p->cfg.D) * p->cfg.D * 2 : 0);
-    if (hpad != nullptr) *hpad = h;
+    L.hpad = take(bf16 ? (size_t)padded_rows(p->cfg.D) * p->cfg.D * 2 : 0);
+    L.repeats = take(bf16 ? (size_t)std::min(C, p->cfg.V) * p->cfg.D * 4 : 0);
     L.total = off;
     return L;
 }
@@ -418,8 +422,7 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
     if (!aligned_to(c.token, 8) || !aligned_to(c.lse, 4) || !aligned_to(c.entropy, 4) ||
         !aligned_to(c.dlogprob, 4) || !aligned_to(c.dentropy, 4) || !aligned_to(c.err_count, 4))
         return FLDCE_ERR_ALIGN;
-    size_t hpad = 0;
-    const Layout L = lp_bwd_layout(h, N, &hpad);
+    const LpBwdLayout L = lp_bwd_layout(h, N);
     if (c.workspace_bytes < L.total) return FLDCE_ERR_WORKSPACE;
     DeviceInfo dev;
     if (int s = check_device(&dev)) return s;
@@ -444,6 +447,7 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
              reinterpret_cast<float*>(ws + L.zy), reinterpret_cast<float*>(ws + L.loss_tok),
              reinterpret_cast<int32_t*>(ws + L.row_y), reinterpret_cast<float*>(ws + L.part_sz),
              nullptr, reinterpret_cast<int32_t*>(ws + L.part_am)};
+    float* repeats = reinterpret_cast<float*>(ws + L.repeats);
     if (bf16 && c.dW != nullptr) k.first = reinterpret_cast<int32_t*>(ws + L.part_ml);
     float* db_part = reinterpret_cast<float*>(ws + L.db_part);
     float* db_acc = reinterpret_cast<float*>(ws + L.db_acc);
@@ -458,7 +462,7 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
         const bool pads = bf16 && pads_rows(rows, D);
         const int64_t map_rows = pads ? padded_rows(D) : rows;
         const int64_t n_pad = pads ? map_rows * (D / 8) : 0;
-        uint4* hp = reinterpret_cast<uint4*>(ws + hpad);
+        uint4* hp = reinterpret_cast<uint4*>(ws + L.hpad);
         const int64_t n_thr = std::max({k.first != nullptr ? std::max<int64_t>(V, 32 * (int64_t)rows)
                                                            : (int64_t)rows, n_pad});
         k_logprob_coef<<<(unsigned)cdiv(n_thr, 256), 256, 0, st>>>(
@@ -511,11 +515,18 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
                         st, rows, r0, DynRows(), lp_max_splits(L.C, D)};
             gg.dh_rest = RowRest{k.y, nullptr, k.res, static_cast<const __nv_bfloat16*>(c.W), (int)V};
             gg.dw_rest = RowRest{k.first, k.next, k.res, reinterpret_cast<const __nv_bfloat16*>(Hc),
-                                 rows};
+                                 rows, repeats, V <= L.C};
             if (c.dH != nullptr)
                 if (int e = gg.dh(mG_k, mW_mn, c.dH)) return e;
-            if (c.dW != nullptr)
+            if (c.dW != nullptr) {
+                if (rows > 1 && c.token != nullptr) {
+                    const unsigned blocks = (unsigned)std::min<int64_t>(rows, 4 * (int64_t)dev.sms);
+                    k_logprob_repeats<<<dim3(blocks, (unsigned)cdiv(D, 1024)), 128, 0, st>>>(
+                        k, rows, reinterpret_cast<const __nv_bfloat16*>(Hc), D, V <= L.C, repeats);
+                    FLDCE_CUDA(cudaGetLastError());
+                }
                 if (int e = gg.dw(mG_mn, mH_mn, c.dW, ci)) return e;
+            }
         } else {
             const float* Hf = reinterpret_cast<const float*>(Hc);
             const float* Wf = static_cast<const float*>(c.W);

@@ -1,0 +1,45 @@
+"""Log-probabilities, alternatives and gradients where they are easily wrong:
+frequent targets, cancelling products, masked weights, rows with nothing left
+and long batches, against the 64-bit definitions of tests/_logprob_ref.py."""
+import math
+
+import pytest
+import torch
+
+from linear_diffusion_cross_b200.logprob import fused_linear_logprobs
+from tests import _logprob_ref as R
+from tests.test_logprob_gpu import close, grads_of, make
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.mark.parametrize("per,targets,D,chunk", [
+    (5, 6, 72, 0), (8, 3, 72, 0), (5, 40, 264, 0), (8, 30, 72, 0), (64, 5, 1032, 0),
+    (256, 3, 72, 0), (300, 1, 520, 0), (64, 12, 72, 256), (700, 2, 2056, 0)])
+def test_rounding_is_given_back_to_frequent_targets(per, targets, D, chunk):
+    """dW of targets that many tokens share: the target's element of a 16-bit G,
+    nine tenths of the way to the middle between two 16-bit numbers, must not
+    cost dW its rounding, whose sum over n tokens of either sign grows as fast
+    as dW itself.  W is zero but for the targets (nearly flat: p = 1 / V)."""
+    N, V = per * targets, 1500
+    x, _, w, _ = make(N, D, V, BF, seed=N)
+    g = torch.Generator(device=DEV).manual_seed(per)
+    ids = torch.randperm(V, device=DEV, generator=g)[:targets]
+    y = ids[torch.randperm(N, device=DEV, generator=g) % targets]
+    keep = torch.zeros(V, 1, device=DEV, dtype=BF)
+    keep[ids] = 1
+    w = w * keep * 2.0 ** -6
+    a = torch.full((N,), (1 + 0.9 * 2.0 ** -8) / (1 - 1 / V), device=DEV)
+    a[torch.rand(N, device=DEV, generator=g) < 0.5] *= -1
+    (_, got), _ = grads_of(x, y, w, None, 1.0, a, None, chunk_n=chunk)
+    _, want, _, A = R.grads(x, y, w, None, 1.0, a, None)
+    rest = A.clone()
+    rest[torch.arange(N, device=DEV), y] = 0                     # what stays rounded
+    u, dz, xa = 2.0 ** -8, R.bound_z(x, w, None, 1.0), x.double().abs()
+    # fp32: p's relative error, every accumulation, the rest's own rounding
+    fp = 4 * dz + 2.0 ** -18 + N * 2.0 ** -23
+    lim = u * want.abs() + u * (1 + u) * (rest.T @ xa) + fp * (A.T @ xa) * (1 + u)
+    err = (got.double() - want).abs()
+    assert bool((err <= lim + 1e-30).all()), float((err / (lim + 1e-30)).max())
