@@ -345,13 +345,17 @@ int fldce_forward(fldce_handle h,
  *                 values in increasing column order
  *   top_logprobs[n] = their z - lse[n]
  *
- * The logits never reach memory.  The order of top_ids is that of the exact
- * dot products (candidates are recomputed in fp64), so it does not depend on
- * N or on how the work is split.  A bias of -inf (or of the type's lowest
- * value) takes a column out: its p is 0.  A row whose every logit is -inf has
- * lse = -inf, entropy 0, logprob -inf and, in the gradient, a row of zeros.
- * Alternatives that do not exist (fewer than top_k logits above -inf) read
- * id -1 and log-probability -inf.  A row with a NaN or +inf logit has NaN
+ * The logits never reach memory.  The columns of top_ids are taken from at
+ * least top_k + 3 that have the largest logits in fp32, and ordered by their
+ * exact dot products (recomputed in fp64).  So they are the exact ones, and do
+ * not depend on N or on how the work is split, unless more than three columns
+ * past the top_k-th come within the fp32 error of it (units of 2^-23 times
+ * sum_d |H W|, about D / 16 + 16 of them in bf16 and D in fp32): which of
+ * those are taken is then fp32's choice.  A bias of -inf (or of the type's
+ * lowest value) takes a column out: its p is 0.  A row whose every logit is
+ * -inf has lse = -inf, entropy 0, logprob -inf and, in the gradient, a row of
+ * zeros.  Alternatives that do not exist (fewer than top_k logits above -inf)
+ * read id -1 and log-probability -inf.  A row with a NaN or +inf logit has NaN
  * results and no meaningful ids.
  *
  * The plan gives dtype, D, V, max_N, logit_scale, ignore_index and, for the

@@ -14,11 +14,11 @@
 //
 // The alternatives' order is decided in 64 bits: every slice keeps its KC best
 // columns by the fp32 accumulator, the merge keeps the KC best of all slices
-// (KC exceeds the k asked for by 3 or more), recomputes in fp64 the dot
-// products of the first k and of those that fp32 cannot tell from the k-th,
-// and sorts by (value, lowest id).  So ids do not depend on the summation
+// (KC exceeds the k asked for by 3 or more), recomputes their dot products in
+// fp64 and sorts by (value, lowest id).  So ids do not depend on the summation
 // order of the matrix instructions, the tile that computed them, or the
-// number of tokens in the call.
+// number of tokens in the call, unless more than KC - k columns past the k-th
+// come within the fp32 error of it: which KC of them are kept is fp32's choice.
 #pragma once
 #include "kernels.cuh"
 
@@ -273,17 +273,16 @@ __device__ __forceinline__ int nibble(uint32_t w, int i) {
 
 constexpr int kDots = 4;             // rows of W per group of dot products
 
-// This thread's share of <x, W_v[j]> (z) and of sum |x_i w_i| (mag), j <
-// kDots, v[j] < 0 being skipped; the block's threads share a row, and four
-// rows' loads are in flight together.  Products of two bf16 (and of 4-bit
-// values) are exact in fp32; products of fp32 are taken in fp64; the sums are
-// in fp64.
+// This thread's share of <x, W_v[j]>, j < kDots, v[j] < 0 being skipped; the
+// block's threads share a row, and four rows' loads are in flight together.
+// Products of two bf16 (and of 4-bit values) are exact in fp32; products of
+// fp32 are taken in fp64; the sums are in fp64.
 template <class T>
 __device__ __forceinline__ void dot_share(const T* __restrict__ x, const HeadWeight& hw,
                                           const int (&v)[kDots], int64_t D, int tid, int threads,
-                                          double (&z)[kDots], float (&mag)[kDots]) {
+                                          double (&z)[kDots]) {
 #pragma unroll
-    for (int j = 0; j < kDots; ++j) { z[j] = 0.0; mag[j] = 0.f; }
+    for (int j = 0; j < kDots; ++j) z[j] = 0.0;
     if constexpr (sizeof(T) == 2) {
         const uint4* xq = reinterpret_cast<const uint4*>(x);
         const int n = (int)(D / 8);
@@ -304,11 +303,8 @@ __device__ __forceinline__ void dot_share(const T* __restrict__ x, const HeadWei
                 for (int j = 0; j < kDots; ++j) {
                     if (v[j] < 0) continue;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float t = f[k] * ((float)nibble(w[j], k) * c[j]);
-                        z[j] += (double)t;
-                        mag[j] += fabsf(t);
-                    }
+                    for (int k = 0; k < 8; ++k)
+                        z[j] += (double)(f[k] * ((float)nibble(w[j], k) * c[j]));
                 }
             }
         } else {
@@ -326,11 +322,7 @@ __device__ __forceinline__ void dot_share(const T* __restrict__ x, const HeadWei
                     float g[8];
                     unpack8(w[j], g);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float t = f[k] * g[k];
-                        z[j] += (double)t;
-                        mag[j] += fabsf(t);
-                    }
+                    for (int k = 0; k < 8; ++k) z[j] += (double)(f[k] * g[k]);
                 }
             }
         }
@@ -340,10 +332,7 @@ __device__ __forceinline__ void dot_share(const T* __restrict__ x, const HeadWei
 #pragma unroll
             for (int j = 0; j < kDots; ++j) {
                 if (v[j] < 0) continue;
-                const double t =
-                    xi * (double)__ldg(static_cast<const float*>(hw.W) + (int64_t)v[j] * D + i);
-                z[j] += t;
-                mag[j] += fabsf((float)t);
+                z[j] += xi * (double)__ldg(static_cast<const float*>(hw.W) + (int64_t)v[j] * D + i);
             }
         }
     }
@@ -361,7 +350,6 @@ struct LpMergeParams {
     int n_parts;
     int64_t D, V, ignore_index;
     float s, c;
-    float dot_err;                   // bound of a logit's fp32 error over sum |x_i w_i|
     const void* H;                   // chunk's hidden states [rows, D]
     HeadWeight hw;
     const void* bias;                // [V] (type of H) or null
@@ -411,10 +399,10 @@ __device__ __forceinline__ uint64_t warp_draw(uint64_t (&key)[n], int lane) {
 // column), and of the r-th of them only the first KC - r entries matter.
 // Warps draw the slices, then the columns, by warp-wide maxima.
 //
-// Dot products in fp64: the given token, the first k candidates, and of the
-// others those that the fp32 values cannot tell from the k-th (their distance
-// is below twice the bound of the fp32 error).  The result is sorted by the
-// fp64 values.
+// Dot products in fp64: the given token and all KC candidates, and the result
+// sorted by them.  (A candidate past the k-th may be any distance below it in
+// fp32 and still be the best, where its products cancel: how far off fp32 is
+// shows only in sum |x_i w_i|, which takes the same loads.)
 //
 // Four warps share a group of dot products.  With few rows a block has four
 // such sets (THREADS = 512): the latency of one row is the kernel's, and one
@@ -435,9 +423,7 @@ __global__ void __launch_bounds__(THREADS) k_logprob_merge(const LpMergeParams p
     __shared__ float cand_v[KA];
     __shared__ int cand_id[KA];
     __shared__ double cand_z[KA + 1];                  // the given token's last
-    __shared__ float cand_abs[KA + 1];
     __shared__ double sm_z[4][KA + 1];
-    __shared__ float sm_mag[4][KA + 1];
     const float4* stats = p.parts.stats + row;
     const size_t ld = p.parts.ld;
     // launched while the kernel before may still run: wait for its results
@@ -562,20 +548,13 @@ __global__ void __launch_bounds__(THREADS) k_logprob_merge(const LpMergeParams p
         for (int j = 0; j < kDots; ++j) any = any || v[j] >= 0;
         if (!any) return;                              // the same for the whole set
         double z[kDots];
-        float mag[kDots];
-        dot_share<T>(x, p.hw, v, p.D, tid & 127, 128, z, mag);
+        dot_share<T>(x, p.hw, v, p.D, tid & 127, 128, z);
 #pragma unroll
         for (int j = 0; j < kDots; ++j) {
             if (v[j] < 0) continue;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                z[j] += __shfl_xor_sync(0xffffffffu, z[j], o);
-                mag[j] += __shfl_xor_sync(0xffffffffu, mag[j], o);
-            }
-            if (lane == 0) {
-                sm_z[warp & 3][slot[j]] = z[j];
-                sm_mag[warp & 3][slot[j]] = mag[j];
-            }
+            for (int o = 16; o > 0; o >>= 1) z[j] += __shfl_xor_sync(0xffffffffu, z[j], o);
+            if (lane == 0) sm_z[warp & 3][slot[j]] = z[j];
         }
     };
     // after a barrier: the logit of a slot that dots() was given
@@ -589,50 +568,23 @@ __global__ void __launch_bounds__(THREADS) k_logprob_merge(const LpMergeParams p
         }
         const double z = (sm_z[0][slot] + sm_z[1][slot]) + (sm_z[2][slot] + sm_z[3][slot]);
         cand_z[slot] = (double)p.s * (z + (double)b);
-        cand_abs[slot] = (sm_mag[0][slot] + sm_mag[1][slot]) +
-                         (sm_mag[2][slot] + sm_mag[3][slot]) + fabsf(b);
     };
-    const int first = KC == 0 ? 0 : p.k;               // slots 0 .. k - 1, then the token's
-    for (int i = set * kDots; i <= first; i += SETS * kDots) {
+    // the slots of the candidates, and the given token's after them
+    for (int i = set * kDots; i <= KC; i += SETS * kDots) {
         int slot[kDots], v[kDots];
 #pragma unroll
         for (int j = 0; j < kDots; ++j) {
-            slot[j] = i + j == first ? KC : i + j;
-            v[j] = i + j > first ? -1 : (i + j == first ? (int)y : cand_id[i + j]);
+            slot[j] = i + j;
+            v[j] = i + j > KC ? -1 : (i + j == KC ? (int)y : cand_id[i + j]);
         }
         dots(slot, v);
     }
     __syncthreads();
-    if (tid <= first) {
-        const int v = tid == first ? (int)y : cand_id[tid];
-        if (v >= 0) finish(tid == first ? KC : tid, v);
+    if (tid <= KC) {
+        const int v = tid == KC ? (int)y : cand_id[tid];
+        if (v >= 0) finish(tid, v);
     }
     __syncthreads();
-    if constexpr (KC > 0) {
-        // a candidate past the k-th is as good as the k-th if their fp32
-        // values differ by less than both may be off
-        float mag = 0.f;
-        for (int i = 0; i < p.k; ++i)
-            if (cand_id[i] >= 0) mag = fmaxf(mag, cand_abs[i]);
-        const float least = cand_v[p.k - 1] - 2.f * p.dot_err * mag;
-        if (cand_v[p.k] >= least && cand_id[p.k] >= 0) {          // seldom
-            for (int i = p.k + set * kDots; i < KC; i += SETS * kDots) {
-                int slot[kDots], v[kDots];
-#pragma unroll
-                for (int j = 0; j < kDots; ++j) {
-                    slot[j] = i + j;
-                    v[j] = i + j < KC && cand_v[i + j] >= least ? cand_id[i + j] : -1;
-                }
-                dots(slot, v);
-            }
-            __syncthreads();
-        }
-        if (tid >= p.k && tid < KC) {
-            if (cand_id[tid] >= 0 && cand_v[tid] >= least) finish(tid, cand_id[tid]);
-            else cand_z[tid] = -CUDART_INF;
-        }
-        __syncthreads();
-    }
     if (warp != 0) return;
 
     // ---- results
@@ -653,12 +605,14 @@ __global__ void __launch_bounds__(THREADS) k_logprob_merge(const LpMergeParams p
     }
     if constexpr (KC > 0) {
         const int id = lane < KC ? cand_id[lane] : -1;
-        const double z = id >= 0 ? cand_z[lane] : -CUDART_INF;
+        // (a NaN ranks last: every rank is taken once, every output written)
+        auto value = [&](int j) { return cand_z[j] == cand_z[j] ? cand_z[j] : -CUDART_INF; };
+        const double z = id >= 0 ? value(lane) : -CUDART_INF;
         int rank = 0;
 #pragma unroll
         for (int j = 0; j < KC; ++j) {
             const int ij = cand_id[j];
-            const double zj = cand_z[j];
+            const double zj = value(j);
             if (ij >= 0 && (zj > z || (zj == z && ij < id))) ++rank;
         }
         const int found = __popc(__ballot_sync(0xffffffffu, id >= 0));

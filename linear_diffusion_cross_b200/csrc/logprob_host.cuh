@@ -293,9 +293,6 @@ int lp_forward(fldce_plan* h, const fldce_logprob_call& call, const LpLayout& L,
         mp.ignore_index = cfg.ignore_index;
         mp.s = cfg.logit_scale;
         mp.c = c;
-        // fp32 accumulation: one ulp per step, in steps of 16 products on the
-        // tensor cores (which align and cut the 16: a few ulp more), 1 otherwise
-        mp.dot_err = (bf16 ? (float)cdiv(D, 16) + 16.f : (float)D) * 1.2e-7f;
         mp.H = Hc;
         mp.hw = hw;
         mp.bias = call.bias;

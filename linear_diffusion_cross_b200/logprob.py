@@ -140,8 +140,10 @@ def fused_linear_logprobs(x: torch.Tensor, token: Optional[torch.Tensor],
 
     z = logit_scale * (x W^T + bias).  A token equal to ``ignore_index``, or
     outside [0, V), has logprob 0 and no gradient through it.  ``top_ids`` are
-    ordered by the exact logits, equal ones by lowest id; a bias of -inf takes
-    an entry out.  ``chunk_n`` (0: the library's choice) bounds the tokens
+    ordered by the exact logits, equal ones by lowest id, among at least
+    ``top_k + 3`` entries that have the largest fp32 logits (so they are the
+    exact best unless more than three others come within the fp32 error of the
+    last); a bias of -inf takes an entry out.  ``chunk_n`` (0: the library's choice) bounds the tokens
     whose logit gradient the backward holds at a time.
     """
     w4 = isinstance(weight, W4Weight)

@@ -43,3 +43,44 @@ def test_rounding_is_given_back_to_frequent_targets(per, targets, D, chunk):
     lim = u * want.abs() + u * (1 + u) * (rest.T @ xa) + fp * (A.T @ xa) * (1 + u)
     err = (got.double() - want).abs()
     assert bool((err <= lim + 1e-30).all()), float((err / (lim + 1e-30)).max())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("N", [2, 20, 40])
+def test_a_cancelling_product_can_be_the_best(N, dtype):
+    """Column 301's products 2^24 and -2^24 swallow its others in 32 bits (0
+    instead of 1.40625); column 7's are small and sum to 0.5."""
+    V, D = 600, 512
+    x = torch.ones(N, D, device=DEV, dtype=dtype)
+    w = torch.zeros(V, D, device=DEV)
+    w[:, 1] = -10.0
+    w[7, 1] = 0.5
+    w[301] = 0.0
+    small = [i for i in range(64, 256) if i % 64 < 32]
+    w[301, small] = 1.875 * 2.0 ** -7
+    w[301, 0], w[301, 256] = 2.0 ** 24, -(2.0 ** 24)
+    w = w.to(dtype)
+    r = fused_linear_logprobs(x, None, w, top_k=1)
+    z = x.double() @ w.double().T
+    assert torch.equal(r.top_ids[:, 0].long(), z.argmax(1)) and int(r.top_ids[0, 0]) == 301
+    for k in (2, 3):
+        r = fused_linear_logprobs(x, None, w, top_k=k)
+        assert r.top_ids[:, :2].tolist() == [[301, 7]] * N
+
+
+@pytest.mark.parametrize("k", [1, 5, 12, 20])
+def test_near_ties_up_to_three_past_k_are_in_exact_order(k):
+    """k + 3 logits that 32 bits cannot tell apart, above all others: exact ids
+    from either side of the token count where the kernels change."""
+    V, g = 900, torch.Generator(device=DEV).manual_seed(k)
+    x = torch.ones(40, 16, device=DEV, dtype=BF)
+    w = torch.zeros(V, 16, device=DEV)
+    at = torch.randperm(V, device=DEV, generator=g)[:k + 3]
+    w[at, 0] = 4096.0
+    w[at, 1] = torch.arange(k + 3, device=DEV).float() * 2.0 ** -14
+    w = w.to(BF)
+    z = x.double() @ w.double().T
+    ids = z.sort(dim=1, descending=True, stable=True).indices[:, :k].int()
+    for n in (1, 9, 17, 32, 33, 40):
+        r = fused_linear_logprobs(x[:n], None, w, top_k=k)
+        assert torch.equal(r.top_ids, ids[:n]), n
