@@ -221,7 +221,6 @@ k_logprob_sweep(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             const int64_t left = p.V - n0;
             if (left <= 0) continue;            // a slice past the vocabulary
             const int ncols = (int)(left < kSliceCols ? left : kSliceCols);
-            const bool edge = p.bias != nullptr || ncols < kSliceCols;   // a may be -inf
             RunningStats rs;
             ThreadTop<KC> tt;
             if constexpr (KC > 0) tt.init(live ? row_floor<KC>(p.parts, m) : CUDART_INF_F);
@@ -259,13 +258,11 @@ k_logprob_sweep(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     float d0, d1;
                     add2(d0, d1, a[i], a[i + 1], -ref, -ref);
                     mul2(d0, d1, d0, d1, c, c);
-                    if (edge) {
-                        d0 = d0 < -1e4f ? -1e4f : d0;
-                        d1 = d1 < -1e4f ? -1e4f : d1;
-                    }
+                    // a may be -inf (a bias, a weight, past the vocabulary):
+                    // 2^d d is 0 then, not 0 * inf (a NaN stays one in 2^d)
                     const float e0 = ex2(d0), e1 = ex2(d1);
                     add2(l0, l1, l0, l1, e0, e1);
-                    fma2(w0, w1, e0, e1, d0, d1, w0, w1);
+                    fma2(w0, w1, e0, e1, fmaxf(d0, -1e4f), fmaxf(d1, -1e4f), w0, w1);
                 }
                 rs.l += l0 + l1;
                 rs.w += w0 + w1;

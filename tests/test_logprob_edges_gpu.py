@@ -84,3 +84,23 @@ def test_near_ties_up_to_three_past_k_are_in_exact_order(k):
     for n in (1, 9, 17, 32, 33, 40):
         r = fused_linear_logprobs(x[:n], None, w, top_k=k)
         assert torch.equal(r.top_ids, ids[:n]), n
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("N", [4, 20, 40, 300])
+def test_weights_of_minus_infinity(N, dtype):
+    # logits of -inf without a bias: one in seven, and all of columns 256..511
+    x, y, w, _ = make(N, 64, 1000, dtype, ignored=0.0)
+    x = x.abs() + 0.125
+    gone = torch.zeros(1000, dtype=torch.bool, device=DEV)
+    gone[::7] = True
+    gone[256:512] = True
+    t = R.bounds(x, torch.where(gone[:, None], 0.0, w.float()), None, 1.0)
+    w[gone, 3] = -math.inf
+    r = fused_linear_logprobs(x, y, w, top_k=5)
+    _, lp, ent, lse, ids, top = R.forward(x, y, w, None, 1.0, 5)
+    close(r.lse, lse, t["lse"], "lse")
+    close(r.logprob, lp, t["logprob"], "logprob")
+    close(r.entropy, ent, t["entropy"], "entropy")
+    assert torch.equal(r.top_ids, ids)
+    close(r.top_logprobs, top, t["lse"], "top_logprobs")
