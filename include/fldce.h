@@ -415,7 +415,8 @@ int fldce_logprob(fldce_handle h, const fldce_logprob_call* call);
 /*
  * fldce_logprob_bwd -- gradients of sum_n dlogprob[n] logprob[n] +
  * dentropy[n] entropy[n]: with a = dlogprob (0 for an ignored token) and
- * e = dentropy,
+ * e = dentropy (both taken as 0 where lse is below -2^23: every column is
+ * masked then, and fp32 holds no differences between them),
  *   G[n,v] = s (p[n,v] (-(a + e entropy[n]) - e log p[n,v]) + a [v = y_n])
  *   dH = G W,  dW = G^T H,  db = sum_n G[n,:].
  * G is rounded once to the dtype, as in the loss's gradient.

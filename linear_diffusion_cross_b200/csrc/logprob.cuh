@@ -688,10 +688,13 @@ __global__ void k_logprob_coef(const int64_t* __restrict__ token, const float* _
     }
     const bool has = y != ignore_index;
     const float L = lse[i];
-    const bool none = L == -CUDART_INF_F;          // every logit -inf: nothing to move
+    // Every entry masked, by -inf or by a large negative value: from 2^23 on a
+    // unit of fp32's last place of lse is 1 or more, and 2^(z - lse) anything up
+    // to NaN.  Nothing to move.
+    const bool none = L < -8388608.f;
     const float a = has && dlp != nullptr && !none ? dlp[i] : 0.f;
     const float e = dent != nullptr && !none ? dent[i] : 0.f;
-    o.lse2[i] = none ? 0.f : L * 1.4426950408889634f;
+    o.lse2[i] = none ? 0.f : L * 1.4426950408889634f;          // (kap = ee = ta = 0 then)
     o.kap[i] = e == 0.f ? -s * a : -s * fmaf(e, entropy[i], a);
     o.ee[i] = s * e * 0.69314718055994530942f;
     o.ta[i] = s * a;

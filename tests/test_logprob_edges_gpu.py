@@ -104,3 +104,18 @@ def test_weights_of_minus_infinity(N, dtype):
     close(r.entropy, ent, t["entropy"], "entropy")
     assert torch.equal(r.top_ids, ids)
     close(r.top_logprobs, top, t["lse"], "top_logprobs")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("N", [3, 40])
+@pytest.mark.parametrize("mask", ["lowest", -1e30, -1e9, -math.inf])
+def test_rows_with_every_entry_masked_move_nothing(N, dtype, mask):
+    # whatever value masks: the gradient is zero, not the NaN or the 2^100 that
+    # exp(z - lse) gives where 32 bits cannot hold the difference
+    x, y, w, b = make(N, 64, 600, dtype, bias=True, ignored=0.0)
+    b[:] = torch.finfo(dtype).min if mask == "lowest" else mask
+    a, e = torch.randn(N, device=DEV), torch.randn(N, device=DEV)
+    got, r = grads_of(x, y, w, b, 1.0, a, e)
+    for t in got:
+        assert not t.any()
+    assert not torch.isnan(r.entropy).any() and not torch.isnan(r.lse).any()
