@@ -358,6 +358,11 @@ int fldce_forward(fldce_handle h,
  * read id -1 and log-probability -inf.  A row with a NaN or +inf logit has NaN
  * results and no meaningful ids.
  *
+ * If a wait inside a kernel runs out (a device error bit, in err_count[1] where
+ * that is given), the rows it concerns are NaN and their ids -1 or some other
+ * column's; gradients are NaN as a whole, and logits of fldce_w4_linear in the
+ * columns whose products were cut short.
+ *
  * The plan gives dtype, D, V, max_N, logit_scale, ignore_index and, for the
  * gradient, chunk_N and the flags DW_FP32, DH_FP32 and DW_ACCUMULATE;
  * label_smoothing is not used.  Plans that are vocabulary shards or have
@@ -531,6 +536,13 @@ int fldce_scale(void* x, int64_t n, int32_t dtype, const float* g, void* stream)
  * Errors: INVALID_ARG (null status), DEVICE, CUDA.
  */
 int fldce_selftest_wait(int64_t limit_ns, int32_t* status, void* stream);
+
+/* fldce_selftest_device_error -- until it is called with 0 again, the
+ * process's calls of fldce_logprob, fldce_logprob_bwd and fldce_w4_linear with
+ * bf16 inputs behave as if a device wait had run out with these error bits
+ * (0 to 255): their results are NaN.
+ * Errors: INVALID_ARG. */
+int fldce_selftest_device_error(int32_t bits);
 
 /* fldce_destroy -- free the plan's host memory (and profiling events).
  * NULL is accepted. */

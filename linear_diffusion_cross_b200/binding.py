@@ -43,7 +43,8 @@ EXPORTS = ("fldce_create", "fldce_workspace_size", "fldce_chunk_size", "fldce_fw
            "fldce_logprob_workspace_size", "fldce_logprob", "fldce_logprob_bwd_workspace_size",
            "fldce_logprob_bwd",
            "fldce_w4_quantize", "fldce_w4_linear",
-           "fldce_scale", "fldce_selftest_wait", "fldce_destroy", "fldce_strerror", "fldce_version")
+           "fldce_scale", "fldce_selftest_wait", "fldce_selftest_device_error",
+           "fldce_destroy", "fldce_strerror", "fldce_version")
 FLDCE_PROF_KINDS = 9
 FLDCE_MAX_TOP_K = 20
 
@@ -204,6 +205,8 @@ def load() -> ctypes.CDLL:
     lib.fldce_w4_linear.restype = ctypes.c_int
     lib.fldce_selftest_wait.argtypes = [_I64, _P, _P]
     lib.fldce_selftest_wait.restype = ctypes.c_int
+    lib.fldce_selftest_device_error.argtypes = [ctypes.c_int32]
+    lib.fldce_selftest_device_error.restype = ctypes.c_int
     lib.fldce_scale.argtypes = [_P, _I64, ctypes.c_int32, _P, _P]
     lib.fldce_scale.restype = ctypes.c_int
     lib.fldce_destroy.argtypes = [_P]
@@ -422,6 +425,10 @@ def fldce_scale(x, n, dtype, g, stream=None) -> int:
 def fldce_selftest_wait(limit_ns: int, status, stream=None) -> int:
     return _check(load().fldce_selftest_wait(int(limit_ns), _ptr(status), _stream(stream)),
                   "fldce_selftest_wait")
+
+
+def fldce_selftest_device_error(bits: int) -> int:
+    return _check(load().fldce_selftest_device_error(int(bits)), "fldce_selftest_device_error")
 
 
 def fldce_destroy(h) -> int:

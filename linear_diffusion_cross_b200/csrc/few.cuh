@@ -86,6 +86,7 @@ struct FewParams {
     float c2;                  // s log2(e)
     LpCoef k;                  // the gradient's row coefficients
     int32_t* err;              // device error bits, or null
+    int broken;                // act as if a wait had run out (the self-test's)
 };
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* m, uint32_t bar,
@@ -458,6 +459,15 @@ k_few(const __grid_constant__ FewParams p) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty_bar(s));
                 if (++s == S) { s = 0; ph ^= 1u; }
+        }
+        if (!ok || p.broken) {
+            // a wait ran out: these rows are NaN, not the sum of what came
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[m][n][e] = CUDART_NAN_F;
         }
         // the tile's logits, the K halves added: lg[token][row]
         auto cell = [&](int m, int n, int e) -> float* {

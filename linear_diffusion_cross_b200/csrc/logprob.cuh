@@ -361,6 +361,7 @@ struct LpMergeParams {
     int32_t* top_ids;                // [rows][k]
     float* top_logprobs;             // [rows][k]
     int32_t* n_err;                  // counts tokens outside [0, V), or null
+    const int32_t* dev_err;          // the sweep's device error bits, or null
 };
 
 constexpr int kMergeKeep = 6;        // slices a thread keeps in registers
@@ -429,6 +430,19 @@ __global__ void __launch_bounds__(THREADS) k_logprob_merge(const LpMergeParams p
     // launched while the kernel before may still run: wait for its results
     // (returns at once after an ordinary launch)
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (p.dev_err != nullptr && *p.dev_err != 0) {
+        // a wait of the sweep ran out: some slices were never written
+        if (tid == 0) {
+            if (p.logprob != nullptr) p.logprob[row] = CUDART_NAN_F;
+            if (p.entropy != nullptr) p.entropy[row] = CUDART_NAN_F;
+            if (p.lse != nullptr) p.lse[row] = CUDART_NAN_F;
+        }
+        if (KC > 0 && tid < p.k) {
+            p.top_ids[(size_t)row * p.k + tid] = -1;
+            p.top_logprobs[(size_t)row * p.k + tid] = CUDART_NAN_F;
+        }
+        return;
+    }
 
     // ---- statistics: a thread's first slices stay in registers between passes
     float4 kept[kMergeKeep];
@@ -508,7 +522,8 @@ __global__ void __launch_bounds__(THREADS) k_logprob_merge(const LpMergeParams p
             const int r = i / KC, e = i - r * KC;
             if (e >= sel_n[r]) continue;
             const float2 t = p.parts.top[((size_t)sel_part[r] * KC + e) * ld + row];
-            ent_key[i] = rank_key(t.x, __float_as_int(t.y));
+            const int id = __float_as_int(t.y);
+            ent_key[i] = id >= 0 && id < p.V ? rank_key(t.x, id) : 0;
         }
         __syncthreads();
         if (warp == 0) {
@@ -622,7 +637,7 @@ __global__ void __launch_bounds__(THREADS) k_logprob_merge(const LpMergeParams p
         }
         if (lane >= found && lane < p.k) {             // fewer logits above -inf than asked for
             p.top_ids[(size_t)row * p.k + lane] = -1;
-            p.top_logprobs[(size_t)row * p.k + lane] = kNegInf;
+            p.top_logprobs[(size_t)row * p.k + lane] = lse == lse ? kNegInf : CUDART_NAN_F;
         }
     }
 }
@@ -653,8 +668,10 @@ __global__ void k_logprob_coef(const int64_t* __restrict__ token, const float* _
                                const float* __restrict__ dent, int rows, int64_t V,
                                int64_t ignore_index, float s, LpCoef o, int32_t* n_err,
                                const uint4* __restrict__ src, int64_t n_src,
-                               uint4* __restrict__ dst, int64_t n_dst) {
+                               uint4* __restrict__ dst, int64_t n_dst, int32_t* dev_err,
+                               int32_t dev_err_init) {
     const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+    if (i == 0 && dev_err != nullptr) *dev_err = dev_err_init;   // the call's first chunk
     // the padded copy of the hidden states, where they need one (see pads_rows)
     if (i < n_dst) dst[i] = i < n_src ? src[i] : make_uint4(0, 0, 0, 0);
     if (o.first != nullptr) {
@@ -867,6 +884,19 @@ __global__ void k_logprob_db(const float* __restrict__ part, int nseg, int64_t V
         float* o = static_cast<float*>(out);
         o[v] = add_out ? o[v] + s : s;
     }
+}
+
+// After a gradient: where a wait of its kernels ran out, tiles were never
+// written or are partial sums, and all of it becomes NaN (bits of ones).
+__global__ void k_logprob_void(const int32_t* __restrict__ dev_err, uint4* dH, int64_t nH, uint4* dW,
+                               int64_t nW, uint16_t* db, int64_t nb) {
+    if (*dev_err == 0) return;
+    const int64_t i0 = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+    const int64_t step = (int64_t)gridDim.x * blockDim.x;
+    const uint4 ones = make_uint4(~0u, ~0u, ~0u, ~0u);
+    for (int64_t i = i0; i < nH; i += step) dH[i] = ones;
+    for (int64_t i = i0; i < nW; i += step) dW[i] = ones;
+    for (int64_t i = i0; i < nb; i += step) db[i] = 0xffff;
 }
 
 // What rounding x to bf16 takes off it (nothing where either is no number).

@@ -23,6 +23,16 @@ constexpr size_t kSmallMap = size_t(128) << 10;
 bool pads_rows(int64_t rows, int64_t D) { return (size_t)rows * D * 2 < kSmallMap; }
 int64_t padded_rows(int64_t D) { return cdiv((int64_t)kSmallMap, 2 * D); }
 
+// fldce_selftest_device_error: the device error bits that calls start from.
+std::atomic<int32_t> g_selftest_dev_err{0};
+
+cudaError_t clear_counters(Counters* cnt, cudaStream_t st) {
+    cudaError_t e = cudaMemsetAsync(cnt, 0, sizeof(Counters), st);
+    const int32_t bits = g_selftest_dev_err.load(std::memory_order_relaxed);
+    if (e == cudaSuccess && bits != 0) e = cudaMemsetAsync(&cnt->dev_err, bits & 0xff, 1, st);
+    return e;
+}
+
 // H [rows, D] bf16 as the maps should see it: itself, or its padded copy in buf.
 cudaError_t pad_rows(const void** H, int64_t* map_rows, void* buf, int64_t rows, int64_t D,
                      cudaStream_t st) {
@@ -199,6 +209,7 @@ cudaError_t launch_few(FewParams& p, const HeadWeight& hw, const __nv_bfloat16* 
     p.tiles = g.tiles;
     p.last_rows = g.last_rows;
     p.hw = hw;
+    p.broken = g_selftest_dev_err.load(std::memory_order_relaxed);
     if constexpr (W4) {
         if (hw.group == 32) return launch_few_lb<true, 0, KC>(p, g, hw, x, D, st);
         if (hw.group == 64) return launch_few_lb<true, 1, KC>(p, g, hw, x, D, st);
@@ -304,6 +315,8 @@ int lp_forward(fldce_plan* h, const fldce_logprob_call& call, const LpLayout& L,
         mp.top_ids = KC > 0 ? call.top_ids + r0 * call.top_k : nullptr;
         mp.top_logprobs = KC > 0 ? call.top_logprobs + r0 * call.top_k : nullptr;
         mp.n_err = call.err_count;
+        // (k_few's statistics are NaN where it failed)
+        mp.dev_err = bf16 && !L.few ? &cnt->dev_err : nullptr;
         // a few rows: the latency of one is the kernel's
         if (!bf16)
             k_logprob_merge<KC, float, 128><<<rows, 128, 0, st>>>(mp);
@@ -378,11 +391,11 @@ int fldce_logprob(fldce_handle h, const fldce_logprob_call* cp) {
     DeviceInfo dev;
     if (int s = check_device(&dev)) return s;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(c.stream);
-    if (c.err_count != nullptr) {
-        Counters* cnt = reinterpret_cast<Counters*>(static_cast<uint8_t*>(c.workspace) + L.cnt);
-        FLDCE_CUDA(cudaMemsetAsync(c.err_count, 0, 8, st));
-        FLDCE_CUDA(cudaMemsetAsync(cnt, 0, sizeof(Counters), st));
-    }
+    Counters* cnt = reinterpret_cast<Counters*>(static_cast<uint8_t*>(c.workspace) + L.cnt);
+    if (c.err_count != nullptr) FLDCE_CUDA(cudaMemsetAsync(c.err_count, 0, 8, st));
+    // (k_few's error bits are only reported: without err_count nobody reads them)
+    if (c.err_count != nullptr || (h->cfg.dtype == FLDCE_BF16 && !L.few))
+        FLDCE_CUDA(clear_counters(cnt, st));
     if (c.N == 0) return FLDCE_OK;
     switch (L.kc) {
         case 0: return lp_forward<0>(h, c, L, dev);
@@ -432,7 +445,7 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
     const float c2 = cfg.logit_scale * 1.4426950408889634f;
     if (c.err_count != nullptr) {
         FLDCE_CUDA(cudaMemsetAsync(c.err_count, 0, 8, st));
-        FLDCE_CUDA(cudaMemsetAsync(cnt, 0, sizeof(Counters), st));
+        FLDCE_CUDA(clear_counters(cnt, st));
     }
     if (N == 0) {
         if (!accum && c.dW != nullptr)
@@ -468,7 +481,8 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
             c.dlogprob != nullptr ? c.dlogprob + r0 : nullptr,
             c.dentropy != nullptr ? c.dentropy + r0 : nullptr, rows, V, cfg.ignore_index,
             cfg.logit_scale, k, c.err_count, reinterpret_cast<const uint4*>(Hc), rows * (D / 8), hp,
-            n_pad);
+            n_pad, ci == 0 ? &cnt->dev_err : nullptr,
+            g_selftest_dev_err.load(std::memory_order_relaxed));
         FLDCE_CUDA(cudaGetLastError());
         prof_mark(h, PK_MERGE, st);
         void* G = ws + L.G;
@@ -564,9 +578,24 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
             prof_mark(h, PK_DB, st);
         }
     }
+    if (bf16) {
+        const size_t dh_elt = (cfg.flags & FLDCE_FLAG_DH_FP32) != 0 ? 4 : 2;
+        k_logprob_void<<<dev.sms, 512, 0, st>>>(
+            &cnt->dev_err, static_cast<uint4*>(c.dH),
+            c.dH != nullptr ? (int64_t)((size_t)N * D * dh_elt / 16) : 0,
+            static_cast<uint4*>(c.dW), c.dW != nullptr ? (int64_t)((size_t)V * D * dw_elt / 16) : 0,
+            static_cast<uint16_t*>(c.db), c.db != nullptr ? (int64_t)(V * dw_elt / 2) : 0);
+        FLDCE_CUDA(cudaGetLastError());
+    }
     if (c.err_count != nullptr)
         FLDCE_CUDA(cudaMemcpyAsync(c.err_count + 1, &cnt->dev_err, 4, cudaMemcpyDeviceToDevice,
                                    st));
+    return FLDCE_OK;
+}
+
+int fldce_selftest_device_error(int32_t bits) {
+    if (bits < 0 || bits > 0xff) return FLDCE_ERR_INVALID_ARG;
+    g_selftest_dev_err.store(bits, std::memory_order_relaxed);
     return FLDCE_OK;
 }
 

@@ -6,7 +6,9 @@ import math
 import pytest
 import torch
 
+from linear_diffusion_cross_b200 import binding as B
 from linear_diffusion_cross_b200.logprob import fused_linear_logprobs
+from linear_diffusion_cross_b200.w4 import linear_w4, quantize_w4
 from tests import _logprob_ref as R
 from tests.test_logprob_gpu import close, grads_of, make
 
@@ -119,3 +121,65 @@ def test_rows_with_every_entry_masked_move_nothing(N, dtype, mask):
     for t in got:
         assert not t.any()
     assert not torch.isnan(r.entropy).any() and not torch.isnan(r.lse).any()
+
+
+@pytest.fixture
+def device_error():
+    B.fldce_selftest_device_error(1)
+    yield
+    B.fldce_selftest_device_error(0)
+
+
+@pytest.mark.parametrize("N", [3, 20, 40])
+def test_a_wait_that_ran_out_gives_nan(N, device_error):
+    # not sums of the stages that came, nor what the memory held before
+    x, y, w, b = make(N, 64, 3001, BF, bias=True, ignored=0.0)
+    w4 = quantize_w4(w, 32)
+    e = torch.ones(N, device=DEV)
+    for weight in (w, w4):
+        for k in (0, 1, 8, 20):
+            r = fused_linear_logprobs(x, y, weight, b, top_k=k)
+            for t in (r.logprob, r.entropy, r.lse) + ((r.top_logprobs,) if k else ()):
+                assert torch.isnan(t).all()
+            assert k == 0 or ((r.top_ids >= -1) & (r.top_ids < 3001)).all()
+    assert torch.isnan(linear_w4(x, w4)).all()
+    got, _ = grads_of(x, y, w, b, 1.0, e, e)
+    for t in got:
+        assert torch.isnan(t).all()
+    B.fldce_selftest_device_error(0)
+    got, r = grads_of(x, y, w, b, 1.0, e, e, top_k=3)
+    for t in (*got, *r):
+        assert torch.isfinite(t).all()
+
+
+@pytest.mark.parametrize("N", [3, 40])
+@pytest.mark.parametrize("flags", [0, B.FLDCE_FLAG_DW_FP32 | B.FLDCE_FLAG_DH_FP32])
+def test_a_wait_that_ran_out_is_reported(N, flags, device_error):
+    x, y, w, b = make(N, 64, 501, BF, bias=True, ignored=0.0)
+    h, _ = B.fldce_create(B.FLDCE_BF16, 64, 501, N, flags=flags)
+    nb = max(B.fldce_logprob_workspace_size(h, N, 2), B.fldce_logprob_bwd_workspace_size(h, N))
+    ws = torch.zeros(nb, dtype=torch.uint8, device=DEV)
+    err = torch.zeros(2, dtype=torch.int32, device=DEV)
+    lse, e = torch.zeros(N, device=DEV), torch.ones(N, device=DEV)
+    t = F32 if flags else BF
+    dH, dW, db = (torch.zeros(s, device=DEV, dtype=t) for s in ((N, 64), (501, 64), (501,)))
+    B.fldce_logprob(h, B.make_logprob_call(H=x, W=w, bias=b, N=N, lse=lse, workspace=ws,
+                                           workspace_bytes=nb, err_count=err))
+    assert err.tolist() == [0, 1] and torch.isnan(lse).all()
+    B.fldce_logprob_bwd(h, B.make_logprob_grad_call(
+        H=x, W=w, bias=b, token=y, N=N, lse=e, entropy=e, dlogprob=e, dH=dH, dW=dW, db=db,
+        workspace=ws, workspace_bytes=nb, err_count=err))
+    assert err.tolist() == [0, 1]
+    for g in (dH, dW, db):
+        assert torch.isnan(g).all()
+    B.fldce_destroy(h)
+
+
+@pytest.mark.parametrize("N", [12, 40])
+def test_rows_with_nan_are_nan_in_every_result(N):
+    x, y, w, b = make(N, 64, 600, BF, bias=True, ignored=0.0)
+    x[7, 3] = math.nan
+    r = fused_linear_logprobs(x, y, w, b, top_k=3)
+    for t in (r.logprob, r.entropy, r.lse, r.top_logprobs):
+        assert torch.isnan(t[7]).all() and torch.isfinite(t[:7]).all()
+    assert (r.top_ids[7] == -1).all()
