@@ -365,8 +365,10 @@ template <class Epi>
 cudaError_t launch_simt(const float* A, int64_t sam, int64_t sak, const float* B, int64_t sbn,
                         int64_t sbk, int M, int64_t N, int K, const Epi& epi, cudaStream_t st) {
     if (M <= 0 || N <= 0) return cudaSuccess;
-    dim3 grid((unsigned)cdiv(N, kSimtTile), (unsigned)cdiv(M, kSimtTile));
-    simt_gemm_kernel<Epi><<<grid, 256, 0, st>>>(A, sam, sak, B, sbn, sbk, M, N, K, epi);
+    // one grid dimension: the second ends at 65535 tiles
+    const int64_t tiles = cdiv(N, kSimtTile) * cdiv(M, kSimtTile);
+    if (tiles > (int64_t(1) << 31) - 1) return cudaErrorInvalidConfiguration;
+    simt_gemm_kernel<Epi><<<(unsigned)tiles, 256, 0, st>>>(A, sam, sak, B, sbn, sbk, M, N, K, epi);
     return cudaGetLastError();
 }
 

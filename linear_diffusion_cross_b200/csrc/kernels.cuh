@@ -1288,8 +1288,10 @@ simt_gemm_kernel(const float* __restrict__ A, int64_t sam, int64_t sak,
     __shared__ float As[16][kSimtTile + 4];
     __shared__ float Bs[16][kSimtTile + 4];
     __shared__ float Cs[kSimtTile][kSimtTile + 1];
-    const int m0 = blockIdx.y * kSimtTile;
-    const int64_t n0 = (int64_t)blockIdx.x * kSimtTile;
+    const unsigned tiles_n = (unsigned)((N + kSimtTile - 1) / kSimtTile);
+    const unsigned mt = blockIdx.x / tiles_n, nt = blockIdx.x - mt * tiles_n;
+    const int m0 = (int)mt * kSimtTile;
+    const int64_t n0 = (int64_t)nt * kSimtTile;
     const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
     float acc[4][4] = {};
     // Element i of this thread's four of an operand tile: consecutive threads
@@ -1343,7 +1345,7 @@ simt_gemm_kernel(const float* __restrict__ A, int64_t sam, int64_t sak,
 #pragma unroll
         for (int j = 0; j < 4; ++j) Cs[ty * 4 + i][tx * 4 + j] = acc[i][j];
     __syncthreads();
-    epi(Cs, m0, n0, (int)blockIdx.x);
+    epi(Cs, m0, n0, (int)nt);
 }
 
 }  // namespace fldce

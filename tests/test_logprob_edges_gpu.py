@@ -123,6 +123,27 @@ def test_rows_with_every_entry_masked_move_nothing(N, dtype, mask):
     assert not torch.isnan(r.entropy).any() and not torch.isnan(r.lse).any()
 
 
+def test_fp32_tokens_beyond_a_grid_dimension():
+    # 65535 tiles of 64 rows and some
+    N, D, V = 65535 * 64 + 200, 8, 8
+    x, y, w, b = make(N, D, V, F32, bias=True)
+    r = fused_linear_logprobs(x, y, w, b, top_k=2)
+    a = torch.randn(N, device=DEV)
+    (gx, gw, gb), _ = grads_of(x, y, w, b, 1.0, a, None)
+    for i in (slice(0, 300), slice(N - 300, N)):
+        _, lp, ent, lse, ids, _ = R.forward(x[i], y[i], w, b, 1.0, 2)
+        t = R.bounds(x[i], w, b, 1.0)
+        close(r.lse[i], lse, t["lse"], "lse")
+        close(r.logprob[i], lp, t["logprob"], "logprob")
+        close(r.entropy[i], ent, t["entropy"], "entropy")
+        assert torch.equal(r.top_ids[i], ids)
+        dH, _, _, A = R.grads(x[i], y[i], w, b, 1.0, a[i], None)
+        lim = R.grad_bounds(x[i], w, A, dH, dH.new_zeros(V, D), dH.new_zeros(V),
+                            R.bound_z(x[i], w, b, 1.0), F32, 300)[0]
+        assert bool(((gx[i].double() - dH).abs() <= lim).all())
+    assert torch.isfinite(gw).all() and torch.isfinite(gb).all()
+
+
 @pytest.fixture
 def device_error():
     B.fldce_selftest_device_error(1)
