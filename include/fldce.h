@@ -411,7 +411,8 @@ typedef struct {
 } fldce_logprob_call;
 
 /* fldce_logprob_workspace_size -- workspace bytes of fldce_logprob for N
- * tokens and top_k alternatives (either kind of weight).
+ * tokens and top_k alternatives (either kind of weight); fewer tokens need no
+ * more.
  * Errors: INVALID_ARG, UNSUPPORTED (plan). */
 int fldce_logprob_workspace_size(fldce_handle h, int64_t N, int32_t top_k, size_t* bytes);
 
@@ -458,7 +459,8 @@ typedef struct {
 
 int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* call);
 
-/* fldce_logprob_bwd_workspace_size -- workspace bytes of fldce_logprob_bwd.
+/* fldce_logprob_bwd_workspace_size -- workspace bytes of fldce_logprob_bwd;
+ * fewer tokens need no more.
  * Errors: INVALID_ARG, UNSUPPORTED (plan). */
 int fldce_logprob_bwd_workspace_size(fldce_handle h, int64_t N, size_t* bytes);
 

@@ -88,6 +88,11 @@ int lp_max_splits(int64_t C, int64_t D) {
     const int64_t part = (int64_t)round_up((size_t)C, 256) * D * 4;
     return (int)std::max<int64_t>(kMaxKSplits, std::min<int64_t>(kLpSplits, kLpSplitBytes / part));
 }
+// Room for that many partials, without the steps of the division: it grows with C.
+size_t lp_split_bytes(int64_t C, int64_t D) {
+    const int64_t part = (int64_t)round_up((size_t)C, 256) * D * 4;
+    return (size_t)std::max(kMaxKSplits * part, std::min(kLpSplits * part, kLpSplitBytes));
+}
 
 struct LpBwdLayout : Layout {
     size_t hpad, repeats;
@@ -115,7 +120,7 @@ LpBwdLayout lp_bwd_layout(const fldce_plan* p, int64_t N) {
     L.part_am = take(bf16 ? C * 4 : 0);
     L.part_ml = take(bf16 ? (size_t)p->cfg.V * 4 : 0);
     L.G = take(round_up((size_t)C, 32) * p->Vpad * p->elt);
-    L.dh_acc = take(bf16 ? (size_t)lp_max_splits(C, p->cfg.D) * round_up((size_t)C, 256) * p->cfg.D * 4 : 0);
+    L.dh_acc = take(bf16 ? lp_split_bytes(C, p->cfg.D) : 0);
     const bool acc = (L.nchunks > 1 || (dw_accumulate(p) && N > 0)) && !dw_out_fp32(p);
     L.dw_acc = take(acc ? (size_t)p->cfg.V * p->cfg.D * 4 : 0);
     L.db_part = take((size_t)kLpColsumSegs * p->cfg.V * 4);
