@@ -19,7 +19,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import binding as B
-from .module import _dtype_code
+from .module import _dtype_code, refuse_forward_mode
 from .w4 import W4Weight, check_w4_input, dense, on_device_of, raw_stream
 
 _MAX_N = (1 << 31) - 1
@@ -163,6 +163,8 @@ def fused_linear_logprobs(x: torch.Tensor, token: Optional[torch.Tensor],
     if not 0 <= top_k <= min(B.FLDCE_MAX_TOP_K, V):
         raise ValueError(f"top_k {top_k} is not in 0..{min(B.FLDCE_MAX_TOP_K, V)}")
     _dtype_code(x.dtype)
+    if not w4:
+        refuse_forward_mode(x, weight, bias)
     if not x.is_cuda:
         raise RuntimeError("the fused log-probabilities run on CUDA tensors only")
     dev = x.device

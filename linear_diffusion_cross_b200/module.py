@@ -24,8 +24,16 @@ from __future__ import annotations
 from typing import Optional
 
 import torch
+from torch.autograd import forward_ad
 
 from . import binding as B
+
+
+def refuse_forward_mode(*tensors: Optional[torch.Tensor]):
+    """Raise for dual tensors: the kernels get addresses, and a tangent would be lost."""
+    for t in tensors:
+        if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+            raise NotImplementedError("forward-mode derivatives are not supported")
 
 
 class _PlanCache:
@@ -117,6 +125,7 @@ def fused_linear_cross_entropy_loss(x: torch.Tensor, target: torch.Tensor,
     if target.shape[0] != x.shape[0] or (p_mask is not None and p_mask.shape[0] != x.shape[0]):
         raise ValueError(f"x={tuple(x.shape)}, target={tuple(target.shape)}, "
                          f"p_mask={None if p_mask is None else tuple(p_mask.shape)}")
+    refuse_forward_mode(x, weight, bias, p_mask)
     if not x.is_cuda:
         raise RuntimeError("the fused linear diffusion cross-entropy runs on CUDA tensors only")
     _dtype_code(x.dtype)

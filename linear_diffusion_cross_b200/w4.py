@@ -15,7 +15,7 @@ from typing import Optional
 import torch
 
 from . import binding as B
-from .module import _dtype_code
+from .module import _dtype_code, refuse_forward_mode
 
 GROUP_SIZES = (32, 64, 128)
 
@@ -124,6 +124,7 @@ def check_w4_input(x: torch.Tensor, weight: W4Weight, bias: Optional[torch.Tenso
         raise ValueError(f"bias {tuple(bias.shape)} {bias.dtype} does not match weight")
     if torch.is_grad_enabled() and (x.requires_grad or (bias is not None and bias.requires_grad)):
         raise RuntimeError("a 4-bit weight has no gradient path: call it under torch.no_grad()")
+    refuse_forward_mode(x, bias)
 
 
 def linear_w4(x: torch.Tensor, weight: W4Weight, bias: Optional[torch.Tensor] = None,

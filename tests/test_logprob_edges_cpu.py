@@ -1,8 +1,16 @@
 """Host-side edges of the log-probability and 4-bit entry points (no GPU needed)."""
 import pytest
+import torch
+from torch.autograd import forward_ad
 
 from linear_diffusion_cross_b200 import binding as B
 from linear_diffusion_cross_b200 import build as _build
+from linear_diffusion_cross_b200.logprob import fused_linear_logprobs
+from linear_diffusion_cross_b200.module import (FusedLinearDiffusionCrossEntropyLoss,
+                                                fused_linear_cross_entropy_loss)
+from linear_diffusion_cross_b200.w4 import W4Weight, linear_w4
+
+BF = torch.bfloat16
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -32,3 +40,37 @@ def test_fewer_tokens_need_no_larger_workspace(D, V, chunk, dtype):
         got = [size(n) for n in ns]
         assert got == sorted(got), [(n, a, b) for n, a, b in zip(ns[1:], got, got[1:]) if b < a]
     B.fldce_destroy(h)
+
+
+def _heads():
+    w4 = W4Weight(torch.zeros(10, 16, dtype=torch.uint8), torch.zeros(10, 1, dtype=BF), 32)
+    y, p = torch.zeros(4, dtype=torch.int64), torch.ones(4)
+    return {
+        "logprobs": lambda x, w, b: fused_linear_logprobs(x, y, w, b).logprob,
+        "logprobs-w4": lambda x, w, b: fused_linear_logprobs(x, y, w4, b).logprob,
+        "linear-w4": lambda x, w, b: linear_w4(x, w4, b),
+        "loss": lambda x, w, b: fused_linear_cross_entropy_loss(x, y, w, b),
+        "loss-module": lambda x, w, b: FusedLinearDiffusionCrossEntropyLoss()(x, y, w, b, p_mask=p),
+    }
+
+
+@pytest.mark.parametrize("head", ["logprobs", "logprobs-w4", "linear-w4", "loss", "loss-module"])
+@pytest.mark.parametrize("which", [0, 1, 2])
+def test_forward_mode_is_refused(head, which):
+    if which == 1 and "w4" in head:
+        pytest.skip("no weight to differentiate")
+    args = [torch.zeros(4, 32, dtype=BF), torch.zeros(10, 32, dtype=BF), torch.zeros(10, dtype=BF)]
+    call = _heads()[head]
+    with forward_ad.dual_level():
+        dual = list(args)
+        dual[which] = forward_ad.make_dual(args[which], torch.ones_like(args[which]))
+        with pytest.raises(NotImplementedError):
+            call(*dual)
+        with pytest.raises(RuntimeError, match="CUDA"):          # nothing dual: as ever
+            call(*args)
+
+    def f(t):
+        return call(*(t if i == which else a for i, a in enumerate(args)))
+
+    with pytest.raises(NotImplementedError):
+        torch.func.jvp(f, (args[which],), (torch.ones_like(args[which]),))
