@@ -23,20 +23,47 @@ from .module import _dtype_code, refuse_forward_mode
 from .w4 import W4Weight, check_w4_input, dense, on_device_of, raw_stream
 
 _MAX_N = (1 << 31) - 1
-_HANDLES = {}
 _INTS = frozenset((torch.int64, torch.int32, torch.int16, torch.int8, torch.uint8))
 
 
-def _handle(dtype: torch.dtype, D: int, V: int, logit_scale: float, ignore_index: int,
-            chunk_n: int) -> int:
-    """A plan's host state (no device memory), one per configuration."""
-    key = (dtype, D, V, logit_scale, ignore_index, chunk_n)
-    h = _HANDLES.get(key)
-    if h is None:
-        h, _ = B.fldce_create(_dtype_code(dtype), D, V, _MAX_N, chunk_N=chunk_n,
-                              logit_scale=logit_scale, ignore_index=ignore_index)
-        h = _HANDLES.setdefault(key, h)
-    return h
+class _Plan:
+    """A plan's host state (no device memory), freed with the last reference."""
+
+    __slots__ = ("handle", "_sizes")
+
+    def __init__(self, dtype: torch.dtype, D: int, V: int, logit_scale: float, ignore_index: int,
+                 chunk_n: int):
+        self.handle = None
+        self._sizes = {}
+        self.handle, _ = B.fldce_create(_dtype_code(dtype), D, V, _MAX_N, chunk_N=chunk_n,
+                                        logit_scale=logit_scale, ignore_index=ignore_index)
+
+    def __del__(self):
+        if self.handle is not None:
+            try:
+                B.fldce_destroy(self.handle)
+            except Exception:      # the interpreter is going down
+                pass
+
+    def _size(self, key: tuple, f, *args) -> int:
+        n = self._sizes.get(key)
+        if n is None:
+            if len(self._sizes) >= 1024:
+                self._sizes.clear()
+            n = self._sizes[key] = f(self.handle, *args)
+        return n
+
+    def workspace_size(self, N: int, top_k: int) -> int:
+        return self._size((N, top_k), B.fldce_logprob_workspace_size, N, top_k)
+
+    def bwd_workspace_size(self, N: int) -> int:
+        return self._size((N,), B.fldce_logprob_bwd_workspace_size, N)
+
+
+# The latest configurations' plans.  One that drops out lives on in the calls
+# and autograd graphs that hold it; a logit_scale that changes each step leaves
+# nothing behind.
+_plan = functools.lru_cache(maxsize=64)(_Plan)
 
 
 class LinearLogProbs(NamedTuple):
@@ -49,22 +76,12 @@ class LinearLogProbs(NamedTuple):
     top_logprobs: Optional[torch.Tensor]   # fp32 [..., top_k]
 
 
-@functools.lru_cache(maxsize=4096)
-def _workspace_size(h: int, N: int, top_k: int) -> int:
-    return B.fldce_logprob_workspace_size(h, N, top_k)
-
-
-@functools.lru_cache(maxsize=4096)
-def _bwd_workspace_size(h: int, N: int) -> int:
-    return B.fldce_logprob_bwd_workspace_size(h, N)
-
-
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     # (an empty tensor may have no address)
     return None if t is None or t.numel() == 0 else t.data_ptr()
 
 
-def _forward(x, weight, bias, token, h, top_k):
+def _forward(x, weight, bias, token, plan, top_k):
     N = x.shape[0]
     dev = x.device
     f32 = torch.float32
@@ -78,14 +95,14 @@ def _forward(x, weight, bias, token, h, top_k):
             top = torch.empty((N, top_k), dtype=f32, device=dev)
         if N == 0:
             return logprob, entropy, lse, ids, top
-        nbytes = _workspace_size(h, N, top_k)
+        nbytes = plan.workspace_size(N, top_k)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         if isinstance(weight, W4Weight):
             w, w4, scales, group = None, weight.packed.data_ptr(), weight.scales.data_ptr(), \
                 weight.group_size
         else:
             w, w4, scales, group = weight.data_ptr(), None, None, 0
-        B.fldce_logprob(h, B.fldce_logprob_call(
+        B.fldce_logprob(plan.handle, B.fldce_logprob_call(
             x.data_ptr(), w, w4, scales, _ptr(bias), _ptr(token), N, group, top_k, _ptr(logprob),
             entropy.data_ptr(), lse.data_ptr(), _ptr(ids), _ptr(top), ws.data_ptr(), nbytes, None,
             raw_stream(dev)))
@@ -96,10 +113,10 @@ class FusedLinearLogProbsFunction(torch.autograd.Function):
     """log p and entropy with gradients; lse and the alternatives without."""
 
     @staticmethod
-    def forward(ctx, x, weight, bias, token, h, top_k):
-        logprob, entropy, lse, ids, top = _forward(x, weight, bias, token, h, top_k)
+    def forward(ctx, x, weight, bias, token, plan, top_k):
+        logprob, entropy, lse, ids, top = _forward(x, weight, bias, token, plan, top_k)
         ctx.set_materialize_grads(False)
-        ctx.h = h
+        ctx.plan = plan
         ctx.save_for_backward(x, weight, bias, token, lse, entropy)
         ctx.mark_non_differentiable(*(t for t in (lse, ids, top) if t is not None))
         return logprob, entropy, lse, ids, top
@@ -121,9 +138,9 @@ class FusedLinearLogProbsFunction(torch.autograd.Function):
             dH = torch.empty_like(x) if need_x else None
             dW = torch.empty_like(weight) if need_w else None
             db = torch.empty_like(bias) if need_b else None
-            nbytes = _bwd_workspace_size(ctx.h, N)
+            nbytes = ctx.plan.bwd_workspace_size(N)
             ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-            B.fldce_logprob_bwd(ctx.h, B.fldce_logprob_grad_call(
+            B.fldce_logprob_bwd(ctx.plan.handle, B.fldce_logprob_grad_call(
                 _ptr(x), weight.data_ptr(), _ptr(bias), _ptr(token), N, _ptr(lse), _ptr(entropy),
                 _ptr(dlogprob), _ptr(dentropy), _ptr(dH), _ptr(dW), _ptr(db), ws.data_ptr(),
                 nbytes, None, raw_stream(dev)))
@@ -181,12 +198,12 @@ def fused_linear_logprobs(x: torch.Tensor, token: Optional[torch.Tensor],
             token = token.reshape(-1)
         if token.dtype != torch.int64 or not token.is_contiguous():
             token = token.to(torch.int64).contiguous()
-    h = _handle(x.dtype, D, V, float(logit_scale), int(ignore_index), int(chunk_n))
+    plan = _plan(x.dtype, D, V, float(logit_scale), int(ignore_index), int(chunk_n))
     if torch.is_grad_enabled() and not w4 and (
             x2.requires_grad or weight.requires_grad or (bias is not None and bias.requires_grad)):
-        out = FusedLinearLogProbsFunction.apply(x2, weight, bias, token, h, top_k)
+        out = FusedLinearLogProbsFunction.apply(x2, weight, bias, token, plan, top_k)
     else:
-        out = _forward(x2, weight, bias, token, h, top_k)
+        out = _forward(x2, weight, bias, token, plan, top_k)
     if len(lead) != 1:
         out = (*(None if t is None else t.view(lead) for t in out[:3]),
                *(None if t is None else t.view(*lead, top_k) for t in out[3:]))

@@ -1,10 +1,13 @@
 """Host-side edges of the log-probability and 4-bit entry points (no GPU needed)."""
+import gc
+
 import pytest
 import torch
 from torch.autograd import forward_ad
 
 from linear_diffusion_cross_b200 import binding as B
 from linear_diffusion_cross_b200 import build as _build
+from linear_diffusion_cross_b200 import logprob
 from linear_diffusion_cross_b200.logprob import fused_linear_logprobs
 from linear_diffusion_cross_b200.module import (FusedLinearDiffusionCrossEntropyLoss,
                                                 fused_linear_cross_entropy_loss)
@@ -74,3 +77,43 @@ def test_forward_mode_is_refused(head, which):
 
     with pytest.raises(NotImplementedError):
         torch.func.jvp(f, (args[which],), (torch.ones_like(args[which]),))
+
+
+def test_a_changing_scale_leaves_no_plans_behind(monkeypatch):
+    alive = set()
+    create, destroy = B.fldce_create, B.fldce_destroy
+
+    def fldce_create(*a, **kw):
+        h, n = create(*a, **kw)
+        alive.add(h)
+        return h, n
+
+    def fldce_destroy(h):
+        alive.remove(h)
+        return destroy(h)
+
+    monkeypatch.setattr(B, "fldce_create", fldce_create)
+    monkeypatch.setattr(B, "fldce_destroy", fldce_destroy)
+    logprob._plan.cache_clear()
+    held = logprob._plan(BF, 64, 100, 1.0, -100, 0)
+    assert logprob._plan(BF, 64, 100, 1.0, -100, 0) is held
+    for i in range(300):
+        p = logprob._plan(BF, 64, 100, 1.0 + i / 1000, -100, 0)
+        assert p.workspace_size(5, 1) == B.fldce_logprob_workspace_size(p.handle, 5, 1)
+        for n in range(20):
+            assert p.bwd_workspace_size(n) == B.fldce_logprob_bwd_workspace_size(p.handle, n)
+    gc.collect()
+    assert len(alive) <= 66
+    assert held.handle in alive                          # a graph may still need it
+    with pytest.raises(B.FldceError):
+        logprob._plan(BF, 64, 100, 0.0, -100, 0)
+    logprob._plan.cache_clear()
+    del p
+    gc.collect()
+    assert alive == {held.handle}
+    for n in range(3000):
+        held.workspace_size(n, 0)
+    assert len(held._sizes) <= 1024
+    del held
+    gc.collect()
+    assert not alive
