@@ -53,9 +53,10 @@ class on_device_of:
             torch.cuda.set_device(self.back)
 
 
-@dataclasses.dataclass(frozen=True)
+@dataclasses.dataclass(frozen=True, eq=False)
 class W4Weight:
-    """A [V, D] weight in 4 bits: ``packed`` uint8 [V, D/2], ``scales`` bf16 [V, ceil(D/group_size)]."""
+    """A [V, D] weight in 4 bits: ``packed`` uint8 [V, D/2], ``scales`` bf16 [V, ceil(D/group_size)].
+    Two are equal if they are the same object, as parameters are."""
 
     packed: torch.Tensor
     scales: torch.Tensor

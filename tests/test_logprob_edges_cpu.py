@@ -117,3 +117,9 @@ def test_a_changing_scale_leaves_no_plans_behind(monkeypatch):
     del held
     gc.collect()
     assert not alive
+
+
+def test_4_bit_weights_compare_by_identity():
+    make = lambda: W4Weight(torch.zeros(10, 16, dtype=torch.uint8), torch.zeros(10, 1, dtype=BF), 32)
+    a, b = make(), make()
+    assert a == a and a != b and a in [b, a] and len({a, b}) == 2
