@@ -5,6 +5,7 @@ import math
 
 import pytest
 import torch
+import torch.utils.checkpoint
 
 from linear_diffusion_cross_b200 import binding as B
 from linear_diffusion_cross_b200.logprob import fused_linear_logprobs
@@ -204,3 +205,77 @@ def test_rows_with_nan_are_nan_in_every_result(N):
     for t in (r.logprob, r.entropy, r.lse, r.top_logprobs):
         assert torch.isnan(t[7]).all() and torch.isfinite(t[:7]).all()
     assert (r.top_ids[7] == -1).all()
+
+
+@pytest.mark.parametrize("N", [6, 70])
+def test_saved_tensor_hooks_and_checkpoints(N):
+    x, y, w, b = make(N, 64, 700, BF, bias=True)
+    e = torch.randn(N, device=DEV)
+    want, _ = grads_of(x, y, w, b, 1.0, e, e)
+    leaves = [t.clone().requires_grad_() for t in (x, w, b)]
+    with torch.autograd.graph.save_on_cpu(pin_memory=True):
+        r = fused_linear_logprobs(leaves[0], y, leaves[1], leaves[2])
+    got = torch.autograd.grad([r.logprob, r.entropy], leaves, [e, e])
+    for p, q in zip(got, want):
+        assert torch.equal(p, q)
+
+    def body(a, c, d):
+        q = fused_linear_logprobs(a, y, c, d)
+        return q.logprob, q.entropy
+
+    out = torch.utils.checkpoint.checkpoint(body, *leaves, use_reentrant=False)
+    got = torch.autograd.grad(out, leaves, [e, e])
+    for p, q in zip(got, want):
+        assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("N", [6, 70])
+def test_autograd_step_captured_in_a_graph(N):
+    x, y, w, b = make(N, 64, 700, BF, bias=True)
+    e = torch.randn(N, device=DEV)
+    want, rw = grads_of(x, y, w, b, 1.0, e, e, top_k=2)
+    leaves = [t.clone().requires_grad_() for t in (x, w, b)]
+
+    def step():
+        r = fused_linear_logprobs(leaves[0], y, leaves[1], leaves[2], top_k=2)
+        return list(torch.autograd.grad([r.logprob, r.entropy], leaves, [e, e])) + [
+            t.detach() for t in r]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step()
+    for _ in range(3):
+        for t in out:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for p, q in zip(out, [*want, *(t.detach() for t in rw)]):
+            assert torch.equal(p, q)
+    # other inputs in the same buffers
+    leaves[0].data.copy_(x.flip(0))
+    g.replay()
+    torch.cuda.synchronize()
+    want, rw = grads_of(x.flip(0), y, w, b, 1.0, e, e, top_k=2)
+    for p, q in zip(out, [*want, *(t.detach() for t in rw)]):
+        assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("N", [5, 90])
+def test_an_ignore_index_inside_the_vocabulary(N):
+    x, y, w, b = make(N, 64, 300, BF, bias=True, ignored=0.0)
+    y[::2] = 0
+    e = torch.randn(N, device=DEV)
+    r = fused_linear_logprobs(x, y, w, b, ignore_index=0)
+    z = torch.where(y == 0, -100, y)
+    q = fused_linear_logprobs(x, z, w, b)
+    for s, t in zip(r[:3], q[:3]):
+        assert torch.equal(s, t)
+    got, _ = grads_of(x, y, w, b, 1.0, e, e, ignore_index=0)
+    want, _ = grads_of(x, z, w, b, 1.0, e, e)
+    for s, t in zip(got, want):
+        assert torch.equal(s, t)
