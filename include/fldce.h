@@ -425,7 +425,10 @@ int fldce_logprob(fldce_handle h, const fldce_logprob_call* call);
  * masked then, and fp32 holds no differences between them),
  *   G[n,v] = s (p[n,v] (-(a + e entropy[n]) - e log p[n,v]) + a [v = y_n])
  *   dH = G W,  dW = G^T H,  db = sum_n G[n,:].
- * G is rounded once to the dtype, as in the loss's gradient.
+ * A bf16 G is held in two bf16 terms in a chunk of up to 16 tokens.  With more
+ * it is rounded once, as in the loss's gradient, but what that takes off the
+ * elements at the targets is given back to dH, dW and db before they are
+ * rounded; the others' roundings stay, also in fp32 outputs.
  *   H, W, bias, token   as given to fldce_logprob (a 16- or 32-bit weight).
  *   lse, entropy        [device, in] [N] fp32, its results (entropy may be
  *                       NULL without dentropy).

@@ -83,6 +83,7 @@ struct FewParams {
     void* out;                 // [n_tok][V] (gradient: bf16, rows ldo apart)
     int out_bf16;
     int64_t ldo;
+    int two_terms;             // the gradient in two terms, 2 n_tok rows
     float c2;                  // s log2(e)
     LpCoef k;                  // the gradient's row coefficients
     int32_t* err;              // device error bits, or null
@@ -517,11 +518,14 @@ k_few(const __grid_constant__ FewParams p) {
                 a[j] = i < rows ? src[i] + bias[j] : kNegInf;
             }
             if constexpr (KC == -2) {
+                // bf16; in two terms, what that took off goes to row n_tok + tok
                 const float L2 = p.k.lse2[tok], kap = p.k.kap[tok], ee = p.k.ee[tok];
                 const float ta = p.k.ta[tok];
                 const int64_t y = p.k.y[tok];
                 const bool dead = kap == 0.f && ee == 0.f && ta == 0.f;
                 __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + (int64_t)tok * p.ldo + v0;
+                __nv_bfloat16* o2 = o + (int64_t)p.n_tok * p.ldo;
+                const bool two = p.two_terms != 0;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int i = 32 * (slice + wpt * j) + lane;
@@ -530,10 +534,13 @@ k_few(const __grid_constant__ FewParams p) {
                     if (dead) gr = 0.f;
                     else if (v0 + i == y) {
                         gr += ta;
-                        p.k.res[tok] = bf16_rest(gr);
-                        if (p.k.first != nullptr) atomicMin(p.k.first + y, tok);
+                        if (!two) {
+                            p.k.res[tok] = bf16_rest(gr);
+                            if (p.k.first != nullptr) atomicMin(p.k.first + y, tok);
+                        }
                     }
                     o[i] = __float2bfloat16_rn(gr);
+                    if (two) o2[i] = __float2bfloat16_rn(bf16_rest(gr));
                 }
             } else if constexpr (KC < 0) {
                 const int64_t o = (int64_t)tok * p.V + v0;

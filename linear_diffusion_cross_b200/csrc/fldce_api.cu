@@ -331,7 +331,7 @@ cudaError_t launch_colsum(const void* G, bool g_bf16, int64_t ldg, int rows, int
 // dst = sum of k fp32 partials `stride` floats apart (bf16 or fp32 out).
 cudaError_t launch_sum_splits(const float* part, int64_t stride, int k, void* dst, bool to_bf16,
                               int64_t n, int sms, cudaStream_t st, const RowRest& rest = RowRest{},
-                              int64_t D = 8) {
+                              int64_t D = 8, int64_t fold = 0) {
     const int64_t n8 = n / 8;
     if (n8 == 0) return cudaSuccess;
     const int blocks = (int)std::min<int64_t>(cdiv(n8, 256), 8 * (int64_t)sms);
@@ -340,13 +340,17 @@ cudaError_t launch_sum_splits(const float* part, int64_t stride, int k, void* ds
     auto* of = static_cast<float*>(dst);
     if (rest.first != nullptr) {
         if (to_bf16)
-            k_sum_splits<__nv_bfloat16, true><<<blocks, 256, 0, st>>>(part, stride, k, ob, n8, rest, d8);
+            k_sum_splits<__nv_bfloat16, true>
+                <<<blocks, 256, 0, st>>>(part, stride, k, ob, n8, rest, d8, fold);
         else
-            k_sum_splits<float, true><<<blocks, 256, 0, st>>>(part, stride, k, of, n8, rest, d8);
+            k_sum_splits<float, true>
+                <<<blocks, 256, 0, st>>>(part, stride, k, of, n8, rest, d8, fold);
     } else if (to_bf16) {
-        k_sum_splits<__nv_bfloat16, false><<<blocks, 256, 0, st>>>(part, stride, k, ob, n8, rest, d8);
+        k_sum_splits<__nv_bfloat16, false>
+            <<<blocks, 256, 0, st>>>(part, stride, k, ob, n8, rest, d8, fold);
     } else {
-        k_sum_splits<float, false><<<blocks, 256, 0, st>>>(part, stride, k, of, n8, rest, d8);
+        k_sum_splits<float, false>
+            <<<blocks, 256, 0, st>>>(part, stride, k, of, n8, rest, d8, fold);
     }
     return cudaGetLastError();
 }
@@ -508,6 +512,8 @@ int check_device(DeviceInfo* d) {
     } while (0)
 
 // The two bf16 gradient products of one chunk of `rows` tokens from its G.
+// With fold_tokens > 0, G is the sum of two bf16 terms: rows 0 .. fold_tokens
+// - 1 and the as many below them, `rows` in all; H's rows come twice to match.
 struct GradGemm {
     fldce_plan* h;
     const Layout* L;
@@ -522,6 +528,7 @@ struct GradGemm {
     // What rounding took off G, given back (first null: nothing is).
     RowRest dh_rest{};
     RowRest dw_rest{};
+    int fold_tokens = 0;
 
     // dH = G W (K = V).  When one pass over the tiles leaves many SMs
     // idle in its last round, the vocabulary is split into k ranges;
@@ -546,7 +553,8 @@ struct GradGemm {
         float* part = reinterpret_cast<float*>(ws + L->dh_acc);
         const int split_rows = (int)round_up((size_t)rows, 256);
         void* dHc = static_cast<uint8_t*>(dH) + (size_t)r0 * D * (dh_fp32 ? 4 : 2);
-        if (ks > 1) {
+        const bool partials = ks > 1 || fold_tokens > 0;
+        if (partials) {
             if (!set_store(&hp, WS_STORE, part, D, (int64_t)ks * split_rows, 4))
                 return FLDCE_ERR_CUDA;
             hp.split_rows = split_rows;
@@ -564,9 +572,11 @@ struct GradGemm {
             FLDCE_CUDA((launch_gemm<CfgKM, Epi>(mG_k, mW_mn, rows, D, V, dh_walk, hp,
                                                      &cnt->dev_err, dev->sms, st, dr)));
         prof_mark(h, PK_DH, st);
-        if (ks > 1) {
+        if (partials) {
+            const int tokens = fold_tokens > 0 ? fold_tokens : rows;
             FLDCE_CUDA(launch_sum_splits(part, (int64_t)split_rows * D, ks, dHc, !dh_fp32,
-                                         (int64_t)rows * D, dev->sms, st, dh_rest, D));
+                                         (int64_t)tokens * D, dev->sms, st, dh_rest, D,
+                                         (int64_t)fold_tokens * D));
             prof_mark(h, PK_CONVERT, st);
         }
         return FLDCE_OK;

@@ -1046,20 +1046,28 @@ __global__ void k_f32_to_bf16(const float* __restrict__ src, __nv_bfloat16* __re
 // out[i] = sum_j part[j * stride + i], j = 0 .. k-1 in that order (the K
 // splits of one GEMM), so the result does not depend on which split
 // finished first.  n8 = elements / 8.
+// fold > 0: part[j * stride + fold + i] is added too (a product whose left
+// operand is in two terms, the second one's rows below the first's).
 // REST: each row gets rest X back for its one large element (see RowRest);
 // d8 = columns / 8.
 template <class OutT, bool REST>
 __global__ void k_sum_splits(const float* __restrict__ part, int64_t stride, int k,
-                             OutT* __restrict__ out, int64_t n8, RowRest rest, int d8) {
+                             OutT* __restrict__ out, int64_t n8, RowRest rest, int d8,
+                             int64_t fold) {
     for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n8;
          i += (int64_t)gridDim.x * blockDim.x) {
         float4 a = reinterpret_cast<const float4*>(part)[2 * i];
         float4 b = reinterpret_cast<const float4*>(part)[2 * i + 1];
-        for (int j = 1; j < k; ++j) {
-            const float4* q = reinterpret_cast<const float4*>(part + j * stride);
-            const float4 c = q[2 * i], d = q[2 * i + 1];
+        auto add = [&](const float4* q) {
+            const float4 c = q[2 * i];
+            const float4 d = q[2 * i + 1];
             a.x += c.x; a.y += c.y; a.z += c.z; a.w += c.w;
             b.x += d.x; b.y += d.y; b.z += d.z; b.w += d.w;
+        };
+        if (fold > 0) add(reinterpret_cast<const float4*>(part + fold));
+        for (int j = 1; j < k; ++j) {
+            add(reinterpret_cast<const float4*>(part + j * stride));
+            if (fold > 0) add(reinterpret_cast<const float4*>(part + j * stride + fold));
         }
         if constexpr (REST) {
             const int64_t row = i / d8;

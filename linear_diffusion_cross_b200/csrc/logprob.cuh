@@ -668,12 +668,14 @@ __global__ void k_logprob_coef(const int64_t* __restrict__ token, const float* _
                                const float* __restrict__ dent, int rows, int64_t V,
                                int64_t ignore_index, float s, LpCoef o, int32_t* n_err,
                                const uint4* __restrict__ src, int64_t n_src,
-                               uint4* __restrict__ dst, int64_t n_dst, int32_t* dev_err,
-                               int32_t dev_err_init) {
+                               uint4* __restrict__ dst, int64_t n_dst, int copies,
+                               int32_t* dev_err, int32_t dev_err_init) {
     const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
     if (i == 0 && dev_err != nullptr) *dev_err = dev_err_init;   // the call's first chunk
-    // the padded copy of the hidden states, where they need one (see pads_rows)
-    if (i < n_dst) dst[i] = i < n_src ? src[i] : make_uint4(0, 0, 0, 0);
+    // the padded copy of the hidden states, where they need one (see
+    // pads_rows), or both copies that a G in two terms is multiplied by
+    if (i < n_dst)
+        dst[i] = i < n_src ? src[i] : (i < copies * n_src ? src[i - n_src] : make_uint4(0, 0, 0, 0));
     if (o.first != nullptr) {
         if (i < V) o.first[i] = 0x7fffffff;
         // a warp for every token looks for the next one of the same target

@@ -94,6 +94,15 @@ size_t lp_split_bytes(int64_t C, int64_t D) {
     return (size_t)std::max(kMaxKSplits * part, std::min(kLpSplits * part, kLpSplitBytes));
 }
 
+// G of up to this many tokens is in two bf16 terms, 2 rows each (as many as
+// the 32 rows that G always has room for).  One rounding to bf16 is as large
+// as the results' own: where one or two elements make up most of a row, dH, dW
+// and db of 1 to 16 tokens were up to 2.5 times as far off as once-rounded
+// results (20,000 random steps; now 1.002 times).  Over more tokens it
+// averages out: at most 1.48 times with 17 to 64, so those keep one term.
+// The products' 256-row tiles and their 64-wide K step have the room.
+constexpr int kTwoTermTokens = 16;
+
 struct LpBwdLayout : Layout {
     size_t hpad, repeats;
 };
@@ -125,7 +134,8 @@ LpBwdLayout lp_bwd_layout(const fldce_plan* p, int64_t N) {
     L.dw_acc = take(acc ? (size_t)p->cfg.V * p->cfg.D * 4 : 0);
     L.db_part = take((size_t)kLpColsumSegs * p->cfg.V * 4);
     L.db_acc = take((size_t)p->cfg.V * 4);
-    L.hpad = take(bf16 ? (size_t)padded_rows(p->cfg.D) * p->cfg.D * 2 : 0);
+    L.hpad = take(bf16 ? (size_t)std::max<int64_t>(padded_rows(p->cfg.D), 2 * kTwoTermTokens) * p->cfg.D * 2
+                       : 0);
     L.repeats = take(bf16 ? (size_t)std::min(C, p->cfg.V) * p->cfg.D * 4 : 0);
     L.total = off;
     return L;
@@ -463,7 +473,6 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
              reinterpret_cast<int32_t*>(ws + L.row_y), reinterpret_cast<float*>(ws + L.part_sz),
              nullptr, reinterpret_cast<int32_t*>(ws + L.part_am)};
     float* repeats = reinterpret_cast<float*>(ws + L.repeats);
-    if (bf16 && c.dW != nullptr) k.first = reinterpret_cast<int32_t*>(ws + L.part_ml);
     float* db_part = reinterpret_cast<float*>(ws + L.db_part);
     float* db_acc = reinterpret_cast<float*>(ws + L.db_acc);
     CUtensorMap mW_k, mW_mn;
@@ -474,8 +483,13 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
         const int64_t r0 = ci * h->chunk;
         const int rows = (int)std::min<int64_t>(h->chunk, N - r0);
         const uint8_t* Hc = static_cast<const uint8_t*>(c.H) + (size_t)r0 * D * h->elt;
-        const bool pads = bf16 && pads_rows(rows, D);
-        const int64_t map_rows = pads ? padded_rows(D) : rows;
+        const bool few = bf16 && rows <= kFewTokens, two = bf16 && rows <= kTwoTermTokens;
+        const int g_rows = two ? 2 * rows : rows;       // (H's rows twice to match)
+        const bool pads = bf16 && (two || pads_rows(rows, D));
+        const int64_t map_rows =
+            pads_rows(g_rows, D) ? std::max<int64_t>(padded_rows(D), g_rows) : g_rows;
+        k.first = bf16 && !two && c.dW != nullptr ? reinterpret_cast<int32_t*>(ws + L.part_ml)
+                                                  : nullptr;
         const int64_t n_pad = pads ? map_rows * (D / 8) : 0;
         uint4* hp = reinterpret_cast<uint4*>(ws + L.hpad);
         const int64_t n_thr = std::max({k.first != nullptr ? std::max<int64_t>(V, 32 * (int64_t)rows)
@@ -486,7 +500,7 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
             c.dlogprob != nullptr ? c.dlogprob + r0 : nullptr,
             c.dentropy != nullptr ? c.dentropy + r0 : nullptr, rows, V, cfg.ignore_index,
             cfg.logit_scale, k, c.err_count, reinterpret_cast<const uint4*>(Hc), rows * (D / 8), hp,
-            n_pad, ci == 0 ? &cnt->dev_err : nullptr,
+            n_pad, two ? 2 : 1, ci == 0 ? &cnt->dev_err : nullptr,
             g_selftest_dev_err.load(std::memory_order_relaxed));
         FLDCE_CUDA(cudaGetLastError());
         prof_mark(h, PK_MERGE, st);
@@ -499,21 +513,22 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
             if (!make_store_map(&gp.gmap, G, V, round_up((size_t)rows, 32), h->Vpad, 2) ||
                 !make_map(&mH_k, Hm, D, map_rows, D, 64, 128) ||
                 !make_map(&mH_mn, Hm, D, map_rows, D, 64, 64) ||
-                !make_map(&mG_k, G, V, rows, h->Vpad, 64, 128) ||
-                !make_map(&mG_mn, G, V, rows, h->Vpad, 64, 64))
+                !make_map(&mG_k, G, V, g_rows, h->Vpad, 64, 128) ||
+                !make_map(&mG_mn, G, V, g_rows, h->Vpad, 64, 64))
                 return FLDCE_ERR_CUDA;
             gp.c = c2;
             gp.V = V;
             gp.rows = rows;
             gp.k = k;
             gp.bias = static_cast<const __nv_bfloat16*>(c.bias);
-            if (rows <= kFewTokens) {
+            if (few) {
                 FewParams fp{};
                 fp.V = V;
                 fp.bias = gp.bias;
                 fp.n_tok = rows;
                 fp.out = G;
                 fp.ldo = h->Vpad;
+                fp.two_terms = two ? 1 : 0;
                 fp.c2 = c2;
                 fp.k = k;
                 fp.err = &cnt->dev_err;
@@ -528,14 +543,18 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
             }
             prof_mark(h, PK_G, st);
             GradGemm gg{h,  &L,   ws, cnt,       &dev,
-                        st, rows, r0, DynRows(), lp_max_splits(L.C, D)};
-            gg.dh_rest = RowRest{k.y, nullptr, k.res, static_cast<const __nv_bfloat16*>(c.W), (int)V};
-            gg.dw_rest = RowRest{k.first, k.next, k.res, reinterpret_cast<const __nv_bfloat16*>(Hc),
-                                 rows, repeats, V <= L.C};
+                        st, g_rows, r0, DynRows(), lp_max_splits(L.C, D)};
+            if (two) {
+                gg.fold_tokens = rows;
+            } else {
+                gg.dh_rest = RowRest{k.y, nullptr, k.res, static_cast<const __nv_bfloat16*>(c.W), (int)V};
+                gg.dw_rest = RowRest{k.first, k.next, k.res, reinterpret_cast<const __nv_bfloat16*>(Hc),
+                                     rows, repeats, V <= L.C};
+            }
             if (c.dH != nullptr)
                 if (int e = gg.dh(mG_k, mW_mn, c.dH)) return e;
             if (c.dW != nullptr) {
-                if (rows > 1 && c.token != nullptr) {
+                if (!two && c.token != nullptr) {
                     const unsigned blocks = (unsigned)std::min<int64_t>(rows, 4 * (int64_t)dev.sms);
                     k_logprob_repeats<<<dim3(blocks, (unsigned)cdiv(D, 1024)), 128, 0, st>>>(
                         k, rows, reinterpret_cast<const __nv_bfloat16*>(Hc), D, V <= L.C, repeats);
@@ -564,11 +583,11 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
             }
         }
         if (c.db != nullptr) {
-            int nseg = (int)std::min<int64_t>(kLpColsumSegs, cdiv(rows, 32));
+            int nseg = (int)std::min<int64_t>(kLpColsumSegs, cdiv(g_rows, 32));
             if (bf16) {
                 const dim3 grid((unsigned)cdiv(V, 512), (unsigned)nseg);
                 k_logprob_colsum<<<grid, 128, 0, st>>>(static_cast<const __nv_bfloat16*>(G),
-                                                       h->Vpad, rows, V, (int)cdiv(rows, nseg),
+                                                       h->Vpad, g_rows, V, (int)cdiv(g_rows, nseg),
                                                        db_part);
                 FLDCE_CUDA(cudaGetLastError());
             } else {
@@ -577,7 +596,7 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
             }
             const bool last = ci + 1 == L.nchunks;
             k_logprob_db<<<(unsigned)cdiv(V, 256), 256, 0, st>>>(
-                db_part, nseg, V, k.y, k.res, bf16 ? rows : 0, db_acc, ci > 0 ? 1 : 0,
+                db_part, nseg, V, k.y, k.res, bf16 && !two ? rows : 0, db_acc, ci > 0 ? 1 : 0,
                 last ? c.db : nullptr, dw_out_fp32(h) ? 0 : 1, accum ? 1 : 0);
             FLDCE_CUDA(cudaGetLastError());
             prof_mark(h, PK_DB, st);

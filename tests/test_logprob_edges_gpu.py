@@ -279,3 +279,40 @@ def test_an_ignore_index_inside_the_vocabulary(N):
     want, _ = grads_of(x, z, w, b, 1.0, e, e)
     for s, t in zip(got, want):
         assert torch.equal(s, t)
+
+
+@pytest.mark.parametrize("flags", [0, B.FLDCE_FLAG_DW_FP32 | B.FLDCE_FLAG_DH_FP32,
+                                   B.FLDCE_FLAG_DW_ACCUMULATE])
+@pytest.mark.parametrize("N,D,V,chunk", [(1, 72, 300, 0), (1, 1032, 40000, 0), (2, 264, 700, 0),
+                                         (6, 2056, 5001, 0), (9, 136, 1501, 0), (16, 72, 4099, 0),
+                                         (16, 4104, 700, 0), (47, 264, 700, 16)])
+def test_few_tokens_gradients_are_rounded_once(N, D, V, chunk, flags):
+    """One token's dW is a product of two numbers, and a peaked row's dH a few
+    of W's rows: the rounding of a 16-bit G would be as large an error as the
+    results' own.  G's two terms hold 2^-16."""
+    x, y, w, b = make(N, D, V, BF, seed=V, sigma=4 / math.sqrt(D), bias=True, ignored=0.5)
+    g = torch.Generator(device=DEV).manual_seed(N)
+    a, e = torch.randn(N, device=DEV, generator=g), torch.randn(N, device=DEV, generator=g)
+    r = fused_linear_logprobs(x, y, w, b)
+    h, _ = B.fldce_create(B.FLDCE_BF16, D, V, N, chunk_N=chunk, flags=flags)
+    nb = B.fldce_logprob_bwd_workspace_size(h, N)
+    ws = torch.full((nb + 256,), 255, dtype=torch.uint8, device=DEV)
+    fp32 = flags & B.FLDCE_FLAG_DW_FP32
+    t = F32 if fp32 else BF
+    dH = torch.zeros(N + 1, D, device=DEV, dtype=t)
+    dW, db = torch.zeros(V, D, device=DEV, dtype=t), torch.zeros(V, device=DEV, dtype=t)
+    B.fldce_logprob_bwd(h, B.make_logprob_grad_call(
+        H=x, W=w, bias=b, token=y, N=N, lse=r.lse, entropy=r.entropy, dlogprob=a, dentropy=e,
+        dH=dH, dW=dW, db=db, workspace=ws, workspace_bytes=nb))
+    want = R.grads(x, y, w, b, 1.0, a, e)
+    A = want[3]
+    u = 2.0 ** -24 if fp32 else 2.0 ** -8
+    eps = 2.0 ** -16 + 4 * R.bound_z(x, w, b, 1.0) + 2.0 ** -18
+    xa, wa = x.double().abs(), w.double().abs()
+    for got, ref, big, n in ((dH[:N], want[0], A @ wa, V), (dW, want[1], A.T @ xa, N),
+                             (db, want[2], A.sum(0), N)):
+        lim = u * ref.abs() + (eps + n * 2.0 ** -23) * big * (1 + u) + 1e-30
+        err = (got.double() - ref).abs()
+        assert bool((err <= lim).all()), float((err / lim).max())
+    assert not dH[N].any() and (ws[nb:] == 255).all()
+    B.fldce_destroy(h)
