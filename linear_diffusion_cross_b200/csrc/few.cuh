@@ -1,10 +1,14 @@
 // few.cuh -- the head's product for few tokens (up to 32 at a time), with a
 // 16-bit or a 4-bit weight: its logits, or their statistics without them.
 //
-// Bound by the bytes of the weight, which every CTA streams once: the
-// vocabulary is cut into one contiguous range of rows per SM (equal to
-// within 8 rows), so every SM reads the same bytes and there is no last
-// round.  A producer thread keeps a ring of TMA boxes in flight (up to 198 KB
+// The weight is streamed once: the vocabulary is cut into one contiguous range
+// of rows per SM, a multiple of 8 rows, so nearly every SM reads the same
+// bytes and there is no last round (the last range gets what is left, 232 of
+// 1032 rows at V = 151936; rounding up to 8 leaves SMs without one where V is
+// small, 73 of 148 at V = 1200).  With 16-bit weights and few tokens the
+// weight's bytes bound it (4 tokens of 2560 x 151936: 125 us, 119 at the
+// measured copy rate); with 4 bits, or more tokens, the instructions do.
+// A producer thread keeps a ring of TMA boxes in flight (up to 198 KB
 // per SM, several times bandwidth x latency) across tile boundaries; 8 or
 // 16 consumer warps turn them into logits with m16n8k16 matrix instructions:
 // vocabulary rows are M and tokens are N, so one token costs an 8-column
@@ -29,7 +33,15 @@
 
 namespace fldce {
 
-constexpr int kFewTokens = 32;          // tokens per pass
+// Tokens per pass, and the most that this kernel takes from the 256-row tiles
+// of a 16-bit weight.  Log-probabilities with one alternative, here against
+// there, in us:  tokens of   2560 x 151936   2048 x 32000   3920 x 159722
+//                       8      137 / 195        37 / 65
+//                      24      160 / 198        41 / 61
+//                      32      174 / 188        44 / 58        244 / 334
+// and the gradient's G:  8     142 / 172        31 / 45
+//                      32      170 / 170        36 / 45        249 / 332
+constexpr int kFewTokens = 32;
 constexpr int kFewRows = 256;           // rows of a tile at most
 constexpr int kFewMaxParts = 160;       // CTAs at most
 
@@ -196,9 +208,7 @@ __device__ __forceinline__ void consumers_sync() {
 }
 
 // KC >= 0: statistics and KC candidates per (CTA, token).  -1: logits.
-// -2: the logits' gradient (as LogprobGEpi, whose 256-row tiles are nearly
-// empty here: G of 32 tokens of 3920 x 159722 takes that kernel 294 us, this
-// one 215 us for 6, the weight's bytes alone 191).
+// -2: the logits' gradient (as LogprobGEpi).
 // LB: log2 of a 4-bit weight's group in 32-element blocks.
 template <bool W4, int LB, int NT, int KC>
 __global__ void __launch_bounds__(FewCfg<W4, LB, NT>::THREADS, 1)
