@@ -123,9 +123,10 @@ def check_w4_input(x: torch.Tensor, weight: W4Weight, bias: Optional[torch.Tenso
         raise TypeError(f"a 4-bit weight takes bfloat16 inputs, got {x.dtype}")
     if bias is not None and (bias.shape != (V,) or bias.dtype != x.dtype):
         raise ValueError(f"bias {tuple(bias.shape)} {bias.dtype} does not match weight")
-    if torch.is_grad_enabled() and (x.requires_grad or (bias is not None and bias.requires_grad)):
+    if torch.is_grad_enabled() and (x.requires_grad or weight.scales.requires_grad or
+                                    (bias is not None and bias.requires_grad)):
         raise RuntimeError("a 4-bit weight has no gradient path: call it under torch.no_grad()")
-    refuse_forward_mode(x, bias)
+    refuse_forward_mode(x, weight.scales, bias)
 
 
 def linear_w4(x: torch.Tensor, weight: W4Weight, bias: Optional[torch.Tensor] = None,

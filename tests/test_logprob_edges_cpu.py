@@ -123,3 +123,14 @@ def test_4_bit_weights_compare_by_identity():
     make = lambda: W4Weight(torch.zeros(10, 16, dtype=torch.uint8), torch.zeros(10, 1, dtype=BF), 32)
     a, b = make(), make()
     assert a == a and a != b and a in [b, a] and len({a, b}) == 2
+
+
+def test_scales_that_want_a_gradient_are_refused():
+    x, y = torch.zeros(4, 32, dtype=BF), torch.zeros(4, dtype=torch.int64)
+    w = W4Weight(torch.zeros(10, 16, dtype=torch.uint8),
+                 torch.zeros(10, 1, dtype=BF).requires_grad_(), 32)
+    for call in (lambda: linear_w4(x, w), lambda: fused_linear_logprobs(x, y, w)):
+        with pytest.raises(RuntimeError, match="gradient"):
+            call()
+        with torch.no_grad(), pytest.raises(RuntimeError, match="CUDA"):
+            call()
