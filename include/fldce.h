@@ -412,7 +412,9 @@ typedef struct {
 
 /* fldce_logprob_workspace_size -- workspace bytes of fldce_logprob for N
  * tokens and top_k alternatives (either kind of weight); fewer tokens need no
- * more.
+ * more.  About N V (16 + 8 c) / 128 bytes with c = 0, 4, 8, 16 or 24 entries
+ * kept for top_k = 0, 1, up to 5, 12 or 20, where that is below 1 GiB; more
+ * tokens are taken in chunks.
  * Errors: INVALID_ARG, UNSUPPORTED (plan). */
 int fldce_logprob_workspace_size(fldce_handle h, int64_t N, int32_t top_k, size_t* bytes);
 
@@ -490,8 +492,9 @@ int fldce_w4_quantize(const void* W, int32_t dtype, int64_t V, int64_t D, int32_
  *   out [device, out] [N, V] of out_dtype (FLDCE_BF16 or FLDCE_FP32);
  *   err_count [device, out, may be NULL] 2 int32: [0] = 0, [1] = device error
  *   bits as for fldce_fwd_bwd.
- * The weight is read once for every few tokens; with many tokens a 16-bit
- * weight and a dense product are faster.
+ * The weight is read once for every 32 tokens.  Up to 32 this is faster than a
+ * dense product with a 16-bit weight (32 tokens of 2560 x 151936: 113 against
+ * 130 us), beyond it is slower (64: 225 against 130 us).
  * Errors: INVALID_ARG, UNSUPPORTED, ALIGN, DEVICE, CUDA.
  */
 int fldce_w4_linear(const void* x, int64_t N, const void* packed, const void* scales, int32_t group,

@@ -1,5 +1,8 @@
 """Log-probabilities of given tokens, entropy and the best alternatives from
-hidden states and the head's weight, without the logits in memory.
+hidden states and the head's weight, without the logits in memory (the
+workspace holds candidates of every slice of the vocabulary instead: 0.08 GB
+for 4096 tokens of 151936 entries, 0.7 GB with 8 alternatives, at most about
+1.1 GB for any number of tokens).
 
 ``fused_linear_logprobs(x, token, weight, ...)`` is what scoring, decoding and
 policy-gradient training ask of the head that ``FusedLinearDiffusionCrossEntropyLoss``
