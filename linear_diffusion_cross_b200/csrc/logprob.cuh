@@ -161,6 +161,7 @@ __device__ __forceinline__ float row_floor(const LpParts& p, int row) {
 // A 64-column slice from a tile of the fp32 CUDA-core GEMM.
 template <int KC>
 struct SimtLogprob {
+    float s;                         // |s|
     float c;
     int neg;
     int64_t V;
@@ -183,8 +184,20 @@ struct SimtLogprob {
             if constexpr (KC > 0)
                 if (a > tt.v[KC - 1]) tt.insert(a, (int)n0 + i);
         }
-        const float ref = rs.rebase(mx, c);
-        for (int i = 0; i < ncols; ++i) rs.add(C[r][i], ref, c);
+        // l by e^(s (a - m)), not 2^(c (a - m)): c's rounding alone would move a
+        // term 15 below the maximum by 1e-6 of itself; summed in fp64, so that
+        // small terms after a large one are not cut 64 times
+        const float ref = mx == -CUDART_INF_F ? 0.f : mx;
+        double l = 0.0, w = 0.0;
+        for (int i = 0; i < ncols; ++i) {
+            const float d = C[r][i] - ref;
+            const float e = expf(d * s);
+            l += (double)e;
+            w += (double)(e * fmaxf(d * c, -1e4f));            // (a NaN is in e)
+        }
+        rs.m = mx;
+        rs.l = (float)l;
+        rs.w = (float)w;
         store_part<KC>(parts, nt, m0 + r, rs, tt);
     }
 };
@@ -487,10 +500,10 @@ __global__ void __launch_bounds__(THREADS) k_logprob_merge(const LpMergeParams p
         for (int j = 0; j < kMergeKeep; ++j) {
             const float4 s = kept[j];
             if (s.x != kNegInf || s.y != 0.f) {        // a slice with a logit (or a NaN)
-                const float d = fmaxf((s.x - mx) * p.c, -1e4f);
-                const double f = (double)exp2f(d);
+                const float d = s.x - mx;
+                const double f = (double)expf(d * fabsf(p.s));
                 l += f * s.y;
-                w += f * ((double)s.z + (double)d * s.y);
+                w += f * ((double)s.z + (double)fmaxf(d * p.c, -1e4f) * s.y);
             }
             key[j] = s.x > floor && __float_as_int(s.w) > 0
                          ? rank_key(s.x, c0 + tid + j * 32 * NW) : 0;
@@ -610,14 +623,31 @@ __global__ void __launch_bounds__(THREADS) k_logprob_merge(const LpMergeParams p
     for (int i = 1; i < NW; ++i) { l += sm_l[i]; w += sm_w[i]; }
     // every logit -inf: lse = -inf, no information in the row
     const bool none = mx == kNegInf && l == 0.0;
+    const double sm = (double)fabsf(p.s) * (double)mx;
     const double lnl = none ? 0.0 : log(l);
-    const double lse = none ? -CUDART_INF : (double)fabsf(p.s) * (double)mx + lnl;
+    const double lse = none ? -CUDART_INF : sm + lnl;
+    // What logarithms of probabilities are taken against: the candidates are
+    // most of a peaked row, and their logits are known exactly now, so their
+    // terms of the sum are replaced.  (A log-probability near 0 is then off like
+    // the rest of the row, not like fp32's lse.  lse itself and the entropy stay
+    // what they are without alternatives.)
+    double lse_z = lse;
+    if constexpr (KC > 0) {
+        double dl = 0.0;
+        if (lane < KC && cand_id[lane] >= 0) {
+            const double t = cand_z[lane] - sm;
+            const double t0 = (double)fabsf(p.s) * ((double)cand_v[lane] - (double)mx);
+            if (fabs(t - t0) <= 1.0) dl = exp(t) - exp(t0);        // (not at infinities)
+        }
+        dl = warp_sum(dl);
+        if (!none && dl != 0.0) lse_z = sm + log(l + dl);
+    }
     if (lane == 0) {
         if (p.lse != nullptr) p.lse[row] = (float)lse;
         if (p.entropy != nullptr)
             p.entropy[row] = none ? 0.f : (float)(lnl - 0.69314718055994530942 * (w / l));
         if (p.logprob != nullptr)
-            p.logprob[row] = y < 0 ? 0.f : (none ? kNegInf : (float)(cand_z[KC] - lse));
+            p.logprob[row] = y < 0 ? 0.f : (none ? kNegInf : (float)(cand_z[KC] - lse_z));
     }
     if constexpr (KC > 0) {
         const int id = lane < KC ? cand_id[lane] : -1;
@@ -634,7 +664,7 @@ __global__ void __launch_bounds__(THREADS) k_logprob_merge(const LpMergeParams p
         const int found = __popc(__ballot_sync(0xffffffffu, id >= 0));
         if (id >= 0 && rank < p.k) {
             p.top_ids[(size_t)row * p.k + rank] = id;
-            p.top_logprobs[(size_t)row * p.k + rank] = (float)(z - lse);
+            p.top_logprobs[(size_t)row * p.k + rank] = (float)(z - lse_z);
         }
         if (lane >= found && lane < p.k) {             // fewer logits above -inf than asked for
             p.top_ids[(size_t)row * p.k + lane] = -1;

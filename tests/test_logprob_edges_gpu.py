@@ -316,3 +316,33 @@ def test_few_tokens_gradients_are_rounded_once(N, D, V, chunk, flags):
         assert bool((err <= lim).all()), float((err / lim).max())
     assert not dH[N].any() and (ws[nb:] == 255).all()
     B.fldce_destroy(h)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32", "w4"])
+@pytest.mark.parametrize("N", [1, 20, 40])
+def test_a_certain_tokens_logprob_is_as_good_as_its_rest(N, kind):
+    """One logit far above the others: its log-probability is -(1 - p) for a 1 - p
+    of about 1e-5, which a lse that is off like the fp32 logit (by 5e-6) would
+    bury.  Only the rest's logits may be off like that."""
+    D, V = 2048, 700
+    x, _, w, _ = make(N, D, V, F32 if kind == "fp32" else BF, seed=N, sigma=0.01)
+    w4 = None
+    if kind == "w4":
+        w4 = quantize_w4(w, 32)
+        w = R.unpack(w4.packed, w4.scales, 32, F32)
+    b = torch.zeros(V, device=DEV, dtype=x.dtype)
+    b[333] = 18.0
+    y = torch.full((N,), 333, device=DEV)
+    r = fused_linear_logprobs(x, y, w4 if w4 is not None else w, b, top_k=1)
+    _, lp, _, lse, ids, top = R.forward(x, y, w, b, 1.0, 1)
+    assert torch.equal(r.top_ids, ids) and (ids == 333).all()
+    rest = -torch.expm1(lp)                              # 1 - p
+    tol = rest * (2 * R.bound_z(x, w, b, 1.0) + 2.0 ** -19) + 2.0 ** -23 * rest + 2.0 ** -45
+    # The sum of exponentials is fp32 within a part of the vocabulary, and each
+    # addition to one that holds the large term (1) is off by at most 2^-24: 16
+    # in a 32-column chunk, 2 that join it, 4 chunks of a slice (the most; up to
+    # 8 + 5 + 5 in the few-token kernel, one rounding in fp32).  Parts join in fp64.
+    tol += 22 * 2.0 ** -24
+    for got, want in ((r.logprob, lp), (r.top_logprobs[:, 0], top[:, 0])):
+        err = (got.double() - want).abs()
+        assert bool((err <= tol).all()), float((err / tol).max())
