@@ -93,6 +93,13 @@ extern "C" {
  * its fp32 partials move 2 D / 256 times the bytes the staged dH reads
  * back, and it ran about twice as long as sweep 2 + dH on B200. */
 #define FLDCE_FLAG_FUSED_DH      0x10u
+/* Log-probabilities only (the loss's entry points refuse such a plan, and it
+ * goes with neither shards nor FUSED_DH nor SKIP_IGNORED): the array `lse` has
+ * 2 N floats, lse rounded and behind all N of them what the rounding took off.
+ * fldce_logprob writes both; fldce_logprob_bwd in fp32 takes their sum, without
+ * which its probabilities carry lse's rounding (2^-21 of p at a lse of 16, and
+ * as much as 1 / (1 - p) times that of p's distance from 1). */
+#define FLDCE_FLAG_LSE_PAIR      0x40u
 
 typedef struct fldce_plan* fldce_handle;
 
@@ -377,8 +384,8 @@ int fldce_forward(fldce_handle h,
  *   token    [device, in, may be NULL] [N] int64: y.  ignore_index, or an id
  *            outside [0, V) (counted in err_count[0]), has logprob 0.
  *   top_k    0 to FLDCE_MAX_TOP_K, at most V.
- *   logprob, entropy, lse  [device, out, each may be NULL] [N] fp32; logprob
- *            needs token.
+ *   logprob, entropy, lse  [device, out, each may be NULL] [N] fp32 (lse with
+ *            LSE_PAIR [2 N]); logprob needs token.
  *   top_ids [device, out] [N, top_k] int32, top_logprobs [N, top_k] fp32;
  *            required when top_k > 0.
  *   workspace  [device] at least fldce_logprob_workspace_size bytes, 256-byte
@@ -432,8 +439,8 @@ int fldce_logprob(fldce_handle h, const fldce_logprob_call* call);
  * elements at the targets is given back to dH, dW and db before they are
  * rounded; the others' roundings stay, also in fp32 outputs.
  *   H, W, bias, token   as given to fldce_logprob (a 16- or 32-bit weight).
- *   lse, entropy        [device, in] [N] fp32, its results (entropy may be
- *                       NULL without dentropy).
+ *   lse, entropy        [device, in] [N] fp32 (lse with LSE_PAIR [2 N]), its
+ *                       results (entropy may be NULL without dentropy).
  *   dlogprob, dentropy  [device, in, each may be NULL = 0] [N] fp32; what
  *                       dlogprob holds at ignored tokens is not read.
  *   dH, dW, db          [device, out] as for fldce_fwd_bwd_ex; each may be

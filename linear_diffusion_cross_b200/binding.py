@@ -34,6 +34,7 @@ FLDCE_FLAG_SKIP_IGNORED = 0x2
 FLDCE_FLAG_DH_FP32 = 0x4
 FLDCE_FLAG_DW_ACCUMULATE = 0x8
 FLDCE_FLAG_FUSED_DH = 0x10
+FLDCE_FLAG_LSE_PAIR = 0x40
 
 # every symbol include/fldce.h declares
 EXPORTS = ("fldce_create", "fldce_workspace_size", "fldce_chunk_size", "fldce_fwd_bwd",

@@ -365,14 +365,14 @@ cudaError_t launch_to_bf16(const float* src, void* dst, int64_t n, bool add, int
     return cudaGetLastError();
 }
 
-template <class Epi>
+template <bool SHORT = false, class Epi>
 cudaError_t launch_simt(const float* A, int64_t sam, int64_t sak, const float* B, int64_t sbn,
                         int64_t sbk, int M, int64_t N, int K, const Epi& epi, cudaStream_t st) {
     if (M <= 0 || N <= 0) return cudaSuccess;
     // one grid dimension: the second ends at 65535 tiles
     const int64_t tiles = cdiv(N, kSimtTile) * cdiv(M, kSimtTile);
     if (tiles > (int64_t(1) << 31) - 1) return cudaErrorInvalidConfiguration;
-    simt_gemm_kernel<Epi><<<(unsigned)tiles, 256, 0, st>>>(A, sam, sak, B, sbn, sbk, M, N, K, epi);
+    simt_gemm_kernel<Epi, SHORT><<<(unsigned)tiles, 256, 0, st>>>(A, sam, sak, B, sbn, sbk, M, N, K, epi);
     return cudaGetLastError();
 }
 
@@ -645,6 +645,7 @@ int run(fldce_handle h, const fldce_call& call, bool backward, int mode = MERGE_
     void* db = call.db;
     if (backward && bias != nullptr && db == nullptr) return FLDCE_ERR_INVALID_ARG;
     if (h != nullptr && h->sharded != (mode != MERGE_LOCAL)) return FLDCE_ERR_INVALID_ARG;
+    if (h != nullptr && (h->cfg.flags & FLDCE_FLAG_LSE_PAIR) != 0) return FLDCE_ERR_UNSUPPORTED;
     if (mode == MERGE_EMIT_STATS && stats_out == nullptr) return FLDCE_ERR_INVALID_ARG;
     if (mode == MERGE_GATHERED && (all_stats == nullptr || n_shards <= 0))
         return FLDCE_ERR_INVALID_ARG;
@@ -986,7 +987,10 @@ int fldce_create(fldce_handle* out, const fldce_config* cfg, size_t* workspace_b
     if (!std::isfinite(cfg->logit_scale) || cfg->logit_scale == 0.f) return FLDCE_ERR_INVALID_ARG;
     if (cfg->dtype != FLDCE_BF16 && cfg->dtype != FLDCE_FP32) return FLDCE_ERR_UNSUPPORTED;
     if ((cfg->flags & ~(FLDCE_FLAG_DW_FP32 | FLDCE_FLAG_SKIP_IGNORED | FLDCE_FLAG_DH_FP32 |
-                        FLDCE_FLAG_DW_ACCUMULATE | FLDCE_FLAG_FUSED_DH)) != 0)
+                        FLDCE_FLAG_DW_ACCUMULATE | FLDCE_FLAG_FUSED_DH | FLDCE_FLAG_LSE_PAIR)) != 0)
+        return FLDCE_ERR_UNSUPPORTED;
+    if ((cfg->flags & FLDCE_FLAG_LSE_PAIR) != 0 &&
+        (cfg->vocab_total > 0 || (cfg->flags & (FLDCE_FLAG_SKIP_IGNORED | FLDCE_FLAG_FUSED_DH)) != 0))
         return FLDCE_ERR_UNSUPPORTED;
     if ((cfg->flags & FLDCE_FLAG_FUSED_DH) != 0 &&
         (cfg->dtype != FLDCE_BF16 || (cfg->flags & FLDCE_FLAG_SKIP_IGNORED) != 0))

@@ -1288,8 +1288,10 @@ struct SimtStore {
 };
 
 // C[m, n] = sum_k A[m*sam + k*sak] * B[n*sbn + k*sbk]
-template <class Epi>
-__global__ void __launch_bounds__(256)
+// SHORT: 16 products at a time are summed by themselves and then added, so that
+// the error grows with K / 16 additions and not with K (one addition in 16 more).
+template <class Epi, bool SHORT>
+__global__ void __launch_bounds__(256, 3)
 simt_gemm_kernel(const float* __restrict__ A, int64_t sam, int64_t sak,
                  const float* __restrict__ B, int64_t sbn, int64_t sbk, int M, int64_t N, int K,
                  Epi epi) {
@@ -1301,7 +1303,7 @@ simt_gemm_kernel(const float* __restrict__ A, int64_t sam, int64_t sak,
     const int m0 = (int)mt * kSimtTile;
     const int64_t n0 = (int64_t)nt * kSimtTile;
     const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float acc[4][4] = {};
+    float acc[4][4] = {}, sum[4][4] = {};
     // Element i of this thread's four of an operand tile: consecutive threads
     // along K where that is contiguous, else along the other dimension.  The
     // next tile's elements are loaded while the current one is multiplied.
@@ -1346,12 +1348,19 @@ simt_gemm_kernel(const float* __restrict__ A, int64_t sam, int64_t sak,
 #pragma unroll
                 for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
         }
+        if constexpr (SHORT) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) { sum[i][j] += acc[i][j]; acc[i][j] = 0.f; }
+        }
         __syncthreads();
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) Cs[ty * 4 + i][tx * 4 + j] = acc[i][j];
+        for (int j = 0; j < 4; ++j)
+            Cs[ty * 4 + i][tx * 4 + j] = SHORT ? sum[i][j] : acc[i][j];
     __syncthreads();
     epi(Cs, m0, n0, (int)nt);
 }

@@ -371,6 +371,7 @@ struct LpMergeParams {
     float* logprob;                  // chunk's outputs, each may be null
     float* entropy;
     float* lse;
+    float* lse_lo;                   // what rounding took off lse, or null
     int32_t* top_ids;                // [rows][k]
     float* top_logprobs;             // [rows][k]
     int32_t* n_err;                  // counts tokens outside [0, V), or null
@@ -450,6 +451,7 @@ __global__ void __launch_bounds__(THREADS) k_logprob_merge(const LpMergeParams p
             if (p.logprob != nullptr) p.logprob[row] = CUDART_NAN_F;
             if (p.entropy != nullptr) p.entropy[row] = CUDART_NAN_F;
             if (p.lse != nullptr) p.lse[row] = CUDART_NAN_F;
+            if (p.lse_lo != nullptr) p.lse_lo[row] = 0.f;
         }
         if (KC > 0 && tid < p.k) {
             p.top_ids[(size_t)row * p.k + tid] = -1;
@@ -644,6 +646,8 @@ __global__ void __launch_bounds__(THREADS) k_logprob_merge(const LpMergeParams p
     }
     if (lane == 0) {
         if (p.lse != nullptr) p.lse[row] = (float)lse;
+        if (p.lse_lo != nullptr)
+            p.lse_lo[row] = isfinite((float)lse) ? (float)(lse - (double)(float)lse) : 0.f;
         if (p.entropy != nullptr)
             p.entropy[row] = none ? 0.f : (float)(lnl - 0.69314718055994530942 * (w / l));
         if (p.logprob != nullptr)
@@ -678,9 +682,12 @@ __global__ void __launch_bounds__(THREADS) k_logprob_merge(const LpMergeParams p
 // e = d/d entropy:
 //   G_v = s ( p_v (-(a + e entropy) - e log p_v) + a [v = y] ).
 // With q = acc c' - lse log2(e) = log2 p_v:  G_v = 2^q (kap - ee q) + ta [v = y].
+// In fp32, whose results show the rounding of lse log2(e) (2^-20 of p at a lse
+// of 16): with r = lse / s rounded and t = s r - lse,
+//   q = s (acc - r) + t = ln p_v,   G_v = e^q (kap - ee q) + ta [v = y].
 // ======================================================================
 struct LpCoef {
-    float* lse2;         // [chunk]
+    float* lse2;         // [chunk]; fp32: r
     float* kap;
     float* ee;
     float* ta;
@@ -690,7 +697,7 @@ struct LpCoef {
     // large an error as the rounding of the results.  dH, dW and db get it
     // back; for dW a column's tokens are chained in increasing order.  (Not
     // where G has two terms.)
-    float* res;
+    float* res;          // (fp32: t instead)
     int32_t* first;      // [V] first token whose target this is (set by the sweep), or huge
     int32_t* next;       // [chunk] next token with this token's target, or rows
 };
@@ -700,7 +707,8 @@ __global__ void k_logprob_coef(const int64_t* __restrict__ token, const float* _
                                const float* __restrict__ dent, int rows, int64_t V,
                                int64_t ignore_index, float s, LpCoef o, int32_t* n_err,
                                const uint4* __restrict__ src, int64_t n_src,
-                               uint4* __restrict__ dst, int64_t n_dst, int copies,
+                               uint4* __restrict__ dst, int64_t n_dst, int copies, bool fp32,
+                               const float* __restrict__ lse_lo,
                                int32_t* dev_err, int32_t dev_err_init) {
     const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
     if (i == 0 && dev_err != nullptr) *dev_err = dev_err_init;   // the call's first chunk
@@ -745,12 +753,20 @@ __global__ void k_logprob_coef(const int64_t* __restrict__ token, const float* _
     const bool none = L < -8388608.f;
     const float a = has && dlp != nullptr && !none ? dlp[i] : 0.f;
     const float e = dent != nullptr && !none ? dent[i] : 0.f;
-    o.lse2[i] = none ? 0.f : L * 1.4426950408889634f;          // (kap = ee = ta = 0 then)
+    // (kap = ee = ta = 0 where there is none)
+    if (fp32) {
+        const double Ld = (double)L + (lse_lo != nullptr ? (double)lse_lo[i] : 0.0);
+        const float r = none ? 0.f : (float)(Ld / s);
+        o.lse2[i] = r;
+        o.res[i] = none ? 0.f : (float)((double)r * s - Ld);
+    } else {
+        o.lse2[i] = none ? 0.f : L * 1.4426950408889634f;
+        o.res[i] = 0.f;
+    }
     o.kap[i] = e == 0.f ? -s * a : -s * fmaf(e, entropy[i], a);
-    o.ee[i] = s * e * 0.69314718055994530942f;
+    o.ee[i] = fp32 ? s * e : s * e * 0.69314718055994530942f;
     o.ta[i] = s * a;
     o.y[i] = has ? (int32_t)y : -1;
-    o.res[i] = 0.f;
 }
 
 // What the tokens of a target from the second on give back to its row of dW:
@@ -1018,7 +1034,7 @@ struct LogprobGEpi {
 };
 
 struct SimtLogprobG {
-    float c;
+    float s;
     int64_t V, ldg;
     int rows;
     LpCoef k;
@@ -1034,7 +1050,9 @@ struct SimtLogprobG {
             const float kap = k.kap[m], ee = k.ee[m], ta = k.ta[m];
             if (v < V && !(kap == 0.f && ee == 0.f && ta == 0.f)) {
                 const float a = C[r][i] + (bias != nullptr ? bias[v] : 0.f);
-                g = lp_grad(fmaf(a, c, -k.lse2[m]), kap, ee);
+                float q = fmaf(a - k.lse2[m], s, k.res[m]);
+                q = q < -1e4f ? -1e4f : q;             // a logit of -inf: p = 0, not 0 * inf
+                g = expf(q) * fmaf(-ee, q, kap);
                 if (v == k.y[m]) g += ta;
             }
             G[(size_t)m * ldg + v] = g;

@@ -306,7 +306,7 @@ int lp_forward(fldce_plan* h, const fldce_logprob_call& call, const LpLayout& L,
             FLDCE_CUDA(launch_sweep<KC>(mH, mW, rows, V, D, sp, &cnt->dev_err, dev.sms, st));
         } else {
             SimtLogprob<KC> e{fabsf(cfg.logit_scale), c, neg, V, rows, static_cast<const float*>(call.bias), parts};
-            FLDCE_CUDA(launch_simt(reinterpret_cast<const float*>(Hc), D, 1,
+            FLDCE_CUDA(launch_simt<true>(reinterpret_cast<const float*>(Hc), D, 1,
                                    static_cast<const float*>(call.W), D, 1, rows, V, (int)D, e,
                                    st));
         }
@@ -327,6 +327,8 @@ int lp_forward(fldce_plan* h, const fldce_logprob_call& call, const LpLayout& L,
         mp.logprob = call.logprob != nullptr ? call.logprob + r0 : nullptr;
         mp.entropy = call.entropy != nullptr ? call.entropy + r0 : nullptr;
         mp.lse = call.lse != nullptr ? call.lse + r0 : nullptr;
+        mp.lse_lo = call.lse != nullptr && (cfg.flags & FLDCE_FLAG_LSE_PAIR) != 0
+                        ? call.lse + N + r0 : nullptr;
         mp.top_ids = KC > 0 ? call.top_ids + r0 * call.top_k : nullptr;
         mp.top_logprobs = KC > 0 ? call.top_logprobs + r0 * call.top_k : nullptr;
         mp.n_err = call.err_count;
@@ -473,6 +475,7 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
              reinterpret_cast<int32_t*>(ws + L.row_y), reinterpret_cast<float*>(ws + L.part_sz),
              nullptr, reinterpret_cast<int32_t*>(ws + L.part_am)};
     float* repeats = reinterpret_cast<float*>(ws + L.repeats);
+    const float* lse_lo = (cfg.flags & FLDCE_FLAG_LSE_PAIR) != 0 ? c.lse + N : nullptr;
     float* db_part = reinterpret_cast<float*>(ws + L.db_part);
     float* db_acc = reinterpret_cast<float*>(ws + L.db_acc);
     CUtensorMap mW_k, mW_mn;
@@ -500,8 +503,8 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
             c.dlogprob != nullptr ? c.dlogprob + r0 : nullptr,
             c.dentropy != nullptr ? c.dentropy + r0 : nullptr, rows, V, cfg.ignore_index,
             cfg.logit_scale, k, c.err_count, reinterpret_cast<const uint4*>(Hc), rows * (D / 8), hp,
-            n_pad, two ? 2 : 1, ci == 0 ? &cnt->dev_err : nullptr,
-            g_selftest_dev_err.load(std::memory_order_relaxed));
+            n_pad, two ? 2 : 1, !bf16, lse_lo != nullptr ? lse_lo + r0 : nullptr,
+            ci == 0 ? &cnt->dev_err : nullptr, g_selftest_dev_err.load(std::memory_order_relaxed));
         FLDCE_CUDA(cudaGetLastError());
         prof_mark(h, PK_MERGE, st);
         void* G = ws + L.G;
@@ -566,19 +569,19 @@ int fldce_logprob_bwd(fldce_handle h, const fldce_logprob_grad_call* cp) {
             const float* Hf = reinterpret_cast<const float*>(Hc);
             const float* Wf = static_cast<const float*>(c.W);
             float* Gf = static_cast<float*>(G);
-            SimtLogprobG ge{c2, V, h->Vpad, rows, k, Gf, static_cast<const float*>(c.bias)};
-            FLDCE_CUDA(launch_simt(Hf, D, 1, Wf, D, 1, rows, V, (int)D, ge, st));
+            SimtLogprobG ge{cfg.logit_scale, V, h->Vpad, rows, k, Gf, static_cast<const float*>(c.bias)};
+            FLDCE_CUDA(launch_simt<true>(Hf, D, 1, Wf, D, 1, rows, V, (int)D, ge, st));
             prof_mark(h, PK_G, st);
             if (c.dH != nullptr) {
                 SimtStore hs{rows, D, D, static_cast<float*>(c.dH) + r0 * D, nullptr, 0};
-                FLDCE_CUDA(launch_simt(Gf, h->Vpad, 1, Wf, 1, D, rows, D, (int)V, hs, st));
+                FLDCE_CUDA(launch_simt<true>(Gf, h->Vpad, 1, Wf, 1, D, rows, D, (int)V, hs, st));
                 prof_mark(h, PK_DH, st);
             }
             if (c.dW != nullptr) {
                 float* dw = static_cast<float*>(c.dW);
                 const int mode = accum ? 2 : (L.nchunks == 1 ? 0 : (ci == 0 ? 1 : 2));
                 SimtStore wsd{(int)V, D, D, dw, dw, mode};
-                FLDCE_CUDA(launch_simt(Gf, 1, h->Vpad, Hf, 1, D, (int)V, D, rows, wsd, st));
+                FLDCE_CUDA(launch_simt<true>(Gf, 1, h->Vpad, Hf, 1, D, (int)V, D, rows, wsd, st));
                 prof_mark(h, PK_DW, st);
             }
         }

@@ -32,14 +32,17 @@ _INTS = frozenset((torch.int64, torch.int32, torch.int16, torch.int8, torch.uint
 class _Plan:
     """A plan's host state (no device memory), freed with the last reference."""
 
-    __slots__ = ("handle", "_sizes")
+    __slots__ = ("handle", "lse_pair", "_sizes")
 
     def __init__(self, dtype: torch.dtype, D: int, V: int, logit_scale: float, ignore_index: int,
                  chunk_n: int):
         self.handle = None
         self._sizes = {}
+        # fp32 gradients would show the rounding of lse
+        self.lse_pair = dtype == torch.float32
         self.handle, _ = B.fldce_create(_dtype_code(dtype), D, V, _MAX_N, chunk_N=chunk_n,
-                                        logit_scale=logit_scale, ignore_index=ignore_index)
+                                        logit_scale=logit_scale, ignore_index=ignore_index,
+                                        flags=B.FLDCE_FLAG_LSE_PAIR if self.lse_pair else 0)
 
     def __del__(self):
         if self.handle is not None:
@@ -85,19 +88,22 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _forward(x, weight, bias, token, plan, top_k):
+    """The five results, and the lse that the backward wants (with what rounding
+    took off it behind it, in fp32)."""
     N = x.shape[0]
     dev = x.device
     f32 = torch.float32
     with on_device_of(x):
         logprob = None if token is None else torch.empty(N, dtype=f32, device=dev)
         entropy = torch.empty(N, dtype=f32, device=dev)
-        lse = torch.empty(N, dtype=f32, device=dev)
+        lse_all = torch.empty(2 * N if plan.lse_pair else N, dtype=f32, device=dev)
+        lse = lse_all[:N] if plan.lse_pair else lse_all
         ids = top = None
         if top_k:
             ids = torch.empty((N, top_k), dtype=torch.int32, device=dev)
             top = torch.empty((N, top_k), dtype=f32, device=dev)
         if N == 0:
-            return logprob, entropy, lse, ids, top
+            return logprob, entropy, lse, ids, top, lse_all
         nbytes = plan.workspace_size(N, top_k)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         if isinstance(weight, W4Weight):
@@ -109,7 +115,7 @@ def _forward(x, weight, bias, token, plan, top_k):
             x.data_ptr(), w, w4, scales, _ptr(bias), _ptr(token), N, group, top_k, _ptr(logprob),
             entropy.data_ptr(), lse.data_ptr(), _ptr(ids), _ptr(top), ws.data_ptr(), nbytes, None,
             raw_stream(dev)))
-    return logprob, entropy, lse, ids, top
+    return logprob, entropy, lse, ids, top, lse_all
 
 
 class FusedLinearLogProbsFunction(torch.autograd.Function):
@@ -117,10 +123,10 @@ class FusedLinearLogProbsFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, weight, bias, token, plan, top_k):
-        logprob, entropy, lse, ids, top = _forward(x, weight, bias, token, plan, top_k)
+        logprob, entropy, lse, ids, top, lse_all = _forward(x, weight, bias, token, plan, top_k)
         ctx.set_materialize_grads(False)
         ctx.plan = plan
-        ctx.save_for_backward(x, weight, bias, token, lse, entropy)
+        ctx.save_for_backward(x, weight, bias, token, lse_all, entropy)
         ctx.mark_non_differentiable(*(t for t in (lse, ids, top) if t is not None))
         return logprob, entropy, lse, ids, top
 
@@ -206,7 +212,7 @@ def fused_linear_logprobs(x: torch.Tensor, token: Optional[torch.Tensor],
             x2.requires_grad or weight.requires_grad or (bias is not None and bias.requires_grad)):
         out = FusedLinearLogProbsFunction.apply(x2, weight, bias, token, plan, top_k)
     else:
-        out = _forward(x2, weight, bias, token, plan, top_k)
+        out = _forward(x2, weight, bias, token, plan, top_k)[:5]
     if len(lead) != 1:
         out = (*(None if t is None else t.view(lead) for t in out[:3]),
                *(None if t is None else t.view(*lead, top_k) for t in out[3:]))

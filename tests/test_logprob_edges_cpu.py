@@ -134,3 +134,20 @@ def test_scales_that_want_a_gradient_are_refused():
             call()
         with torch.no_grad(), pytest.raises(RuntimeError, match="CUDA"):
             call()
+
+
+def test_plans_with_a_pair_of_lse_are_for_log_probabilities():
+    for kw in (dict(vocab_start=0, vocab_total=200), dict(flags=B.FLDCE_FLAG_SKIP_IGNORED),
+               dict(flags=B.FLDCE_FLAG_FUSED_DH)):
+        kw["flags"] = kw.get("flags", 0) | B.FLDCE_FLAG_LSE_PAIR
+        with pytest.raises(B.FldceError):
+            B.fldce_create(B.FLDCE_BF16, 64, 100, 10, **kw)
+    h, _ = B.fldce_create(B.FLDCE_FP32, 64, 100, 10, flags=B.FLDCE_FLAG_LSE_PAIR)
+    a = 1 << 20                                          # never dereferenced: refused first
+    call = B.make_call(H=a, W=a, target=a, N=4, total=1.0, loss=a, workspace=a,
+                       workspace_bytes=1 << 40, stream=0)
+    with pytest.raises(B.FldceError) as e:
+        B.fldce_forward_ex(h, call)
+    assert e.value.status == B.FLDCE_ERR_UNSUPPORTED
+    assert B.fldce_logprob_workspace_size(h, 4, 0) > 0
+    B.fldce_destroy(h)

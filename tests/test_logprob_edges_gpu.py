@@ -346,3 +346,48 @@ def test_a_certain_tokens_logprob_is_as_good_as_its_rest(N, kind):
     for got, want in ((r.logprob, lp), (r.top_logprobs[:, 0], top[:, 0])):
         err = (got.double() - want).abs()
         assert bool((err <= tol).all()), float((err / tol).max())
+
+
+@pytest.mark.parametrize("shift", [0.0, 1000.0])
+@pytest.mark.parametrize("s", [1.0, -0.5])
+def test_fp32_gradients_do_not_show_the_rounding_of_lse(shift, s):
+    """Logits whose products and sums are exact in fp32 (multiples of 2^-6 below
+    2^11), far from 0 and with one or two entries that make up most of a row:
+    what is left is the rounding of probabilities, not that of lse (2^-15 at
+    1000) or of lse log2(e)."""
+    N, D, V = 24, 16, 40
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randint(-2, 3, (N, D), device=DEV, generator=g).float()
+    w = torch.randint(-64, 65, (V, D), device=DEV, generator=g).float() / 64
+    b = torch.randint(-64, 65, (V,), device=DEV, generator=g).float() / 64 + shift / s
+    y = torch.randint(0, V, (N,), device=DEV, generator=g)
+    y[::3] = (s * (x @ w.T + b)).argmax(1)[::3]          # p near 1: a (1 - p) cancels
+    a, e = torch.randn(N, device=DEV, generator=g), torch.randn(N, device=DEV, generator=g)
+    got, _ = grads_of(x, y, w, b, s, a, e)
+    want = R.grads(x, y, w, b, s, a, e)
+    A = want[3]
+    # p: exp 2^-22 and its argument, a difference (2^-24 of up to 2^6) scaled and
+    # shifted (two roundings more, of as much); ln p the same; kap 2^-23, the
+    # product and the sum with a 2^-23 more
+    eps = 2.0 ** -22 + 3 * 64 * 2.0 ** -24 + 2.0 ** -22
+    for t, ref, big, n in ((got[0], want[0], A @ w.double().abs(), V),
+                           (got[1], want[1], A.T @ x.double().abs(), N), (got[2], want[2], A.sum(0), N)):
+        # fp32 sums: at most 16 + n / 16 additions on a term's way
+        lim = (eps + (17 + n / 16) * 2.0 ** -24) * big + 2.0 ** -24 * ref.abs() + 1e-30
+        err = (t.double() - ref).abs()
+        assert bool((err <= lim).all()), float((err / lim).max())
+
+
+def test_lse_pair_writes_two_floats_a_row():
+    x, y, w, b = make(37, 64, 900, F32, bias=True)
+    lse = torch.full((37 * 2 + 3,), 7.0, device=DEV)
+    h, _ = B.fldce_create(B.FLDCE_FP32, 64, 900, 37, flags=B.FLDCE_FLAG_LSE_PAIR)
+    nb = B.fldce_logprob_workspace_size(h, 37, 0)
+    ws = torch.empty(nb, dtype=torch.uint8, device=DEV)
+    B.fldce_logprob(h, B.make_logprob_call(H=x, W=w, bias=b, N=37, lse=lse, workspace=ws,
+                                           workspace_bytes=nb))
+    assert (lse[74:] == 7.0).all()
+    r = fused_linear_logprobs(x, y, w, b)
+    assert torch.equal(lse[:37], r.lse) and r.lse.shape == (37,)
+    assert bool((lse[37:74].abs() <= 2.0 ** -24 * lse[:37].abs()).all()) and lse[37:74].any()
+    B.fldce_destroy(h)
