@@ -352,6 +352,10 @@ int fldce_forward(fldce_handle h,
  *                 values in increasing column order
  *   top_logprobs[n] = their z - lse[n]
  *
+ * With top_k > 0, logprob and top_logprobs are taken against a lse in which the
+ * kept columns' terms are exact (recomputed in fp64), so that those near 0 are
+ * not off like fp32's lse; they differ from z - lse[n] by that much.
+ *
  * The logits never reach memory.  The columns of top_ids are taken from at
  * least top_k + 3 that have the largest logits in fp32, and ordered by their
  * exact dot products (recomputed in fp64).  So they are the exact ones, and do
