@@ -305,7 +305,8 @@ int lp_forward(fldce_plan* h, const fldce_logprob_call& call, const LpLayout& L,
                 c, neg, V, rows, static_cast<const __nv_bfloat16*>(call.bias), parts};
             FLDCE_CUDA(launch_sweep<KC>(mH, mW, rows, V, D, sp, &cnt->dev_err, dev.sms, st));
         } else {
-            SimtLogprob<KC> e{fabsf(cfg.logit_scale), c, neg, V, rows, static_cast<const float*>(call.bias), parts};
+            SimtLogprob<KC> e{fabsf(cfg.logit_scale), c, neg, V, rows,
+                              static_cast<const float*>(call.bias), parts};
             FLDCE_CUDA(launch_simt<true>(reinterpret_cast<const float*>(Hc), D, 1,
                                    static_cast<const float*>(call.W), D, 1, rows, V, (int)D, e,
                                    st));

@@ -169,8 +169,9 @@ def fused_linear_logprobs(x: torch.Tensor, token: Optional[torch.Tensor],
     ordered by the exact logits, equal ones by lowest id, among at least
     ``top_k + 3`` entries that have the largest fp32 logits (so they are the
     exact best unless more than three others come within the fp32 error of the
-    last); a bias of -inf takes an entry out.  ``chunk_n`` (0: the library's choice) bounds the tokens
-    whose logit gradient the backward holds at a time.
+    last); a bias of -inf takes an entry out.  ``chunk_n`` (0: the library's
+    choice) bounds the tokens whose logit gradient the backward holds at a time.
+    Forward-mode derivatives are refused.
     """
     w4 = isinstance(weight, W4Weight)
     if w4:
